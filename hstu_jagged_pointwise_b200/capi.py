@@ -24,6 +24,7 @@ HSTU_F32 = 1
 HSTU_MASK_CAUSAL = 0
 HSTU_MASK_MTGR = 1
 HSTU_MASK_MFALCON_SEQ = 2
+HSTU_MASK_WINDOW = 3
 
 # every symbol the header declares
 EXPORTS = (

@@ -124,6 +124,11 @@ template <int KIND>
 __device__ __forceinline__ int next_visible(const KvItem& s, int t, int n_qt) {
     // causal: once a query tile sees the key tile, every later one does
     if (KIND == HSTU_KIND_CAUSAL && t >= 0) return t + 1 < n_qt ? t + 1 : n_qt;
+    // window: the tiles that see it are one run that starts at the key tile's own
+    if (KIND == HSTU_KIND_WINDOW) {
+        t = t < 0 ? s.n0 / kTileM : t + 1;
+        return t < n_qt && q_class<KIND>(s, t) != 0 ? t : n_qt;
+    }
     for (t++; t < n_qt; t++)
         if (q_class<KIND>(s, t) != 0) break;
     return t;
@@ -149,6 +154,17 @@ __device__ __forceinline__ void diag_sums(const float (&zf)[C], float& dlo, floa
     }
 }
 
+// SiLU(z) and SiLU'(z) / alpha of the window kind for h = z / 2: sig = 1 / (1 + exp(-z)),
+// SiLU = z sig, SiLU' = sig + SiLU (1 - sig).  The exponential and the reciprocal are good to
+// a few fp32 roundings (tanh.approx, used by the other kinds, to 2^-11), which the fp32 bias
+// gradients keep.  A masked h (-5e29) gives sig = 0 exactly.
+__device__ __forceinline__ void silu_both(float h, float inv_alpha, float& a, float& g) {
+    const float z = 2.f * h;
+    const float sg = __fdividef(1.f, 1.f + __expf(-z));
+    a = z * sg;
+    g = fmaf(a, 1.f - sg, sg) * inv_alpha;
+}
+
 // One dense block of 32 keys (lanes) x C queries (along the chunk).  dg points at
 // this lane's diagonal-row entry for the block's first query (later queries sit at
 // decreasing addresses); the row holds half the position bias, the causal mask and,
@@ -161,11 +177,12 @@ __device__ __forceinline__ void diag_sums(const float (&zf)[C], float& dlo, floa
 // Queries go in pairs through packed fp32 arithmetic.  With h = z / 2, t = tanh(h) and
 // p = 1 + t:  SiLU(z) = h + h t = h p  and  2 SiLU'(z) = p + SiLU(z) (1 - t).  SiLU is
 // rounded as in the forward (one fused multiply-add), so A matches the forward's P.
-template <bool TV, int C, bool CONST = false>
+// EXACT (the window kind) takes both from silu_both instead.
+template <bool TV, int C, bool EXACT, bool CONST = false>
 __device__ __forceinline__ void bwd_block(const uint32_t (&sv)[C], const uint32_t (&dp)[C], const float* dg, float c0,
                                           bool pos_diag, float& dlo, float& dhi, const int32_t* qr, int32_t a_j,
                                           const float* rth, int nbm1, float& acc, float* g_rt,
-                                          uint32_t (&pa)[C / 2], uint32_t (&pz)[C / 2]) {
+                                          uint32_t (&pa)[C / 2], uint32_t (&pz)[C / 2], float inv_alpha) {
     int32_t q[C];
     if (TV) {
         const int4* q4 = reinterpret_cast<const int4*>(qr);
@@ -193,10 +210,16 @@ __device__ __forceinline__ void bwd_block(const uint32_t (&sv)[C], const uint32_
             hb.y += rth[tb1];
         }
         const float2 h = fma2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), make_float2(0.5f, 0.5f), hb);
-        const float2 t = make_float2(tanh_approx(h.x), tanh_approx(h.y));
-        const float2 p1 = add2(t, one2);
-        const float2 av = fma2(h, t, h);                                // SiLU(z)
-        const float2 g2 = fma2(av, sub2(one2, t), p1);                 // 2 SiLU'(z)
+        float2 av, g2;
+        if (EXACT) {
+            silu_both(h.x, inv_alpha, av.x, g2.x);
+            silu_both(h.y, inv_alpha, av.y, g2.y);
+        } else {
+            const float2 t = make_float2(tanh_approx(h.x), tanh_approx(h.y));
+            const float2 p1 = add2(t, one2);
+            av = fma2(h, t, h);                                        // SiLU(z)
+            g2 = fma2(av, sub2(one2, t), p1);                         // 2 SiLU'(z)
+        }
         const float2 z2 = mul2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), g2);
         zf[e] = z2.x;
         zf[e + 1] = z2.y;
@@ -329,10 +352,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 const int n_qt = (s.L + kTileM - 1) / kTileM;
                 int t_pf = 0;                              // next query tile to prefetch into L2
-                for (int t = 0; ok && t < n_qt; t++) {
-                    if (q_class<KIND>(s, t) == 0) continue;
+                for (int t = KIND == HSTU_KIND_WINDOW ? s.n0 / kTileM : 0; ok && t < n_qt; t++) {
+                    if (q_class<KIND>(s, t) == 0) {
+                        if (KIND == HSTU_KIND_WINDOW) break;   // the visible tiles are one run
+                        continue;
+                    }
                     if (t_pf <= t) t_pf = t + 1;
-                    while (t_pf < n_qt && q_class<KIND>(s, t_pf) == 0) t_pf++;
+                    while (t_pf < n_qt && q_class<KIND>(s, t_pf) == 0)
+                        t_pf = KIND == HSTU_KIND_WINDOW ? n_qt : t_pf + 1;
                     if (t_pf < n_qt) {
                         for (int pn = 0; pn < kPanels; pn++) {
                             tma_prefetch_2d(&tm_q, s.h * D + pn * 64, s.off0 + t_pf * kTileM);
@@ -628,8 +655,16 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     TimeClass tc;
                     tc.tb_lo = tc.tb_hi = 0;
                     tc.thr = 0;
+                    // window: keys part sinks, part not.  Queries far past such a block see its sinks
+                    // only: the other lanes are switched off (lane_off)
+                    const bool mixed = KIND == HSTU_KIND_WINDOW && ka < s.S && s.S <= ka + 31;
+                    bool lane_off = false;
+                    if (mixed && wcls == 1 && i0 - (ka + 31) >= s.R) {
+                        lane_off = j >= s.S;
+                        wcls = 2;
+                    }
                     const bool dense = wcls != 0 && warp_keys == 32 && i0 + C <= s.L &&
-                                       (KIND == HSTU_KIND_CAUSAL || wcls == 2);
+                                       (KIND == HSTU_KIND_CAUSAL || wcls == 2 || (KIND == HSTU_KIND_WINDOW && !mixed));
                     const int dmin = ka - (i0 + C - 1);  // smallest key - query of the block
                     if (dense) {
                         tc = classify_time(kmin, kmax, qmin, qmax, p.nb);
@@ -645,7 +680,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             if (pm == kPosUniform && tm == kTimeUniform) c0 = 0.5f * s_rp[pidx_u] + tadd;
                             else for (int k = lane; k < C + 31; k += 32) {
                                 const int dl = dmin + k;
-                                const bool masked = KIND == HSTU_KIND_CAUSAL && dl > 0;
+                                const bool masked = (KIND == HSTU_KIND_CAUSAL && dl > 0) ||
+                                                    (KIND == HSTU_KIND_WINDOW && wcls == 1 && (dl > 0 || (ka >= s.S && -dl >= s.R)));
                                 w_diag[k] = masked ? kMaskedHalfBias
                                                    : 0.5f * s_rp[min(max(dl, -(p.P - 1)), p.P - 1) + p.P - 1] + tadd;
                             }
@@ -671,12 +707,17 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tmem_ld_wait(sv);
                         tmem_ld_wait(dp);
                         const float* dg = w_diag + lane + C - 1;
+                        constexpr bool X = KIND == HSTU_KIND_WINDOW;
+                        if (X && lane_off) {
+#pragma unroll
+                            for (int e = 0; e < C; e++) dp[e] = 0u;          // dz = 0: no gradient from this key
+                        }
                         if (pm == kPosUniform && tm == kTimeUniform)
-                            bwd_block<false, C, true>(sv, dp, dg, c0, false, dlo, dhi, w_qrel, a_j, s_rth, nbm1, acc, g_rt, pa, pz);
+                            bwd_block<false, C, X, true>(sv, dp, dg, c0, false, dlo, dhi, w_qrel, a_j, s_rth, nbm1, acc, g_rt, pa, pz, p.inv_alpha);
                         else if (tm == kTimeUniform)
-                            bwd_block<false, C>(sv, dp, dg, c0, pm == kPosDiag, dlo, dhi, w_qrel, a_j, s_rth, nbm1, acc, g_rt, pa, pz);
+                            bwd_block<false, C, X>(sv, dp, dg, c0, pm == kPosDiag, dlo, dhi, w_qrel, a_j, s_rth, nbm1, acc, g_rt, pa, pz, p.inv_alpha);
                         else if (tm >= 0)
-                            bwd_block<true, C>(sv, dp, dg, c0, pm == kPosDiag, dlo, dhi, w_qrel, a_j, s_rth, nbm1, acc, g_rt, pa, pz);
+                            bwd_block<true, C, X>(sv, dp, dg, c0, pm == kPosDiag, dlo, dhi, w_qrel, a_j, s_rth, nbm1, acc, g_rt, pa, pz, p.inv_alpha);
                         else {
                             // element by element (MTGR candidates, ragged edges, int64-wide times)
                             int cur_p = -1, cur_t = -1;
@@ -694,9 +735,15 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                     const int pidx = pos_index(token_pos(KIND, min(i, s.L - 1), s.S, s.R), pos_j, p.P);
                                     const int tb = time_bucket(ts_i, ts_j, p.nb);
                                     const float h = fmaf(__uint_as_float(sv[k]), 0.5f, 0.5f * s_rp[pidx] + s_rth[tb]);
-                                    const float th = tanh_approx(h);
-                                    av[f] = vis ? fmaf(h, th, h) : 0.f;
-                                    const float g2 = fmaf(h, fmaf(-th, th, 1.f), th + 1.f);
+                                    float a, g2;
+                                    if (KIND == HSTU_KIND_WINDOW) {
+                                        silu_both(h, p.inv_alpha, a, g2);
+                                    } else {
+                                        const float th = tanh_approx(h);
+                                        a = fmaf(h, th, h);
+                                        g2 = fmaf(h, fmaf(-th, th, 1.f), th + 1.f);
+                                    }
+                                    av[f] = vis ? a : 0.f;
                                     const float dz = vis ? __uint_as_float(dp[k]) * g2 : 0.f;
                                     zf[k] = dz;
                                     if (KIND != HSTU_KIND_CAUSAL) {
@@ -720,6 +767,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             if (cur_p >= 0 && acc_p != 0.f) red_add_f32(&g_rp[cur_p], acc_p);
                             if (cur_t >= 0 && acc_t != 0.f) red_add_f32(&g_rt[cur_t], acc_t);
                             if (KIND == HSTU_KIND_CAUSAL) diag_sums<C>(zf, dlo, dhi);
+                        }
+                        if (X && lane_off) {
+#pragma unroll
+                            for (int e = 0; e < C / 2; e++) pa[e] = 0u;
                         }
                     }
                     // A^T_h back into TMEM inside the S^T_h columns this warp has read
@@ -783,7 +834,8 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     uint32_t* pk = reinterpret_cast<uint32_t*>(wk);
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
-                        pv[e] = n_done ? pack_bf16x2(2.f * __uint_as_float(vv[2 * e]), 2.f * __uint_as_float(vv[2 * e + 1])) : 0u;
+                        const float vs = KIND == HSTU_KIND_WINDOW ? p.inv_alpha : 2.f;
+                        pv[e] = n_done ? pack_bf16x2(vs * __uint_as_float(vv[2 * e]), vs * __uint_as_float(vv[2 * e + 1])) : 0u;
                         pk[e] = n_done ? pack_bf16x2(__uint_as_float(kv[2 * e]), __uint_as_float(kv[2 * e + 1])) : 0u;
                     }
                     const size_t o = (size_t)(s.off0 + j) * p.ld + (size_t)s.h * D + col;
@@ -882,6 +934,8 @@ cudaError_t launch_attn_bwd_tc(int kind, int d, const CUtensorMap& tq, const CUt
     HSTU_BWD_CASE(HSTU_KIND_CAUSAL, 64)
     HSTU_BWD_CASE(HSTU_KIND_MTGR, 128)
     HSTU_BWD_CASE(HSTU_KIND_MTGR, 64)
+    HSTU_BWD_CASE(HSTU_KIND_WINDOW, 128)
+    HSTU_BWD_CASE(HSTU_KIND_WINDOW, 64)
 #undef HSTU_BWD_CASE
     return cudaErrorInvalidValue;
 }

@@ -87,6 +87,16 @@ __device__ __forceinline__ int kv_class(const Item& s, int t) {
     return tile_class(KIND, s.row0, s.row_end - 1, ka, kb, s.S, s.R);
 }
 
+// A key tile t that no row of the item sees: the last one of the run of such tiles that
+// starts at t, so that the loops over key tiles step over what lies between the sinks and
+// the window, or past the rows.  Other kinds have no such runs worth a rule (t itself).
+template <int KIND>
+__device__ __forceinline__ int skip_kv(const Item& s, int t) {
+    if (KIND != HSTU_KIND_WINDOW) return t;
+    if (t * kTileN >= s.row_end) return s.Lk / kTileN;
+    return max(t, max(s.row0 - s.R + 1, 0) / kTileN - 1);
+}
+
 template <int KIND>
 __device__ __forceinline__ int row_pos(const Item& s, int i) {
     if (KIND == HSTU_KIND_MFALCON) return s.Lk;   // every candidate sits right after its history
@@ -273,9 +283,12 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int n_kt = (s.Lk + kTileN - 1) / kTileN;
                 int t_pf = 0;                              // next key tile to prefetch into L2
                 for (int t = 0; ok && t < n_kt; t++) {
-                    if (kv_class<KIND>(s, t) == 0) continue;
+                    if (kv_class<KIND>(s, t) == 0) {
+                        t = skip_kv<KIND>(s, t);
+                        continue;
+                    }
                     if (t_pf <= t) t_pf = t + 1;
-                    while (t_pf < n_kt && kv_class<KIND>(s, t_pf) == 0) t_pf++;
+                    while (t_pf < n_kt && kv_class<KIND>(s, t_pf) == 0) t_pf = skip_kv<KIND>(s, t_pf) + 1;
                     if (t_pf < n_kt) {
                         for (int pn = 0; pn < kPanels; pn++) {
                             tma_prefetch_2d(&tm_k, s.h * D + pn * 64, s.kv0 + t_pf * kTileN);
@@ -334,14 +347,19 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const Item s = load_item<KIND>(p, it);
                 const int n_kt = (s.Lk + kTileN - 1) / kTileN;
                 int last = -1;
-                for (int t = 0; t < n_kt; t++)
+                for (int t = 0; t < n_kt; t++) {
                     if (kv_class<KIND>(s, t) != 0) last = t;
+                    else t = skip_kv<KIND>(s, t);
+                }
                 ok = mbar_wait(&bars[kQFull], q_use & 1, s_abort, p.dbg.limit);
                 q_use++;
                 tc_fence_after();
                 int n_done = 0;
                 for (int t = 0; ok && t <= last; t++) {
-                    if (kv_class<KIND>(s, t) == 0) continue;
+                    if (kv_class<KIND>(s, t) == 0) {
+                        t = skip_kv<KIND>(s, t);
+                        continue;
+                    }
                     ok = mbar_wait(&bars[kKFull], k_use & 1, s_abort, p.dbg.limit);
                     if (!ok) break;
                     k_use++;
@@ -436,8 +454,10 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int n_kt = (s.Lk + kTileN - 1) / kTileN;
             // column timestamps of this warp's keys, loaded one key tile ahead
             auto next_tile = [&](int tt) {
-                for (tt++; tt < n_kt; tt++)
+                for (tt++; tt < n_kt; tt++) {
                     if (kv_class<KIND>(s, tt) != 0) break;
+                    tt = skip_kv<KIND>(s, tt);
+                }
                 return tt;
             };
             int64_t tj_next[2];
@@ -510,12 +530,17 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                             min(n0 + 63, s.Lk - 1), s.S, s.R);
                 const int r_hi = min(r0 + 31, s.row_end - 1);
                 // every row of the block is a candidate sharing one position
-                const bool rows_shared = KIND == HSTU_KIND_MFALCON || (KIND != HSTU_KIND_CAUSAL && r0 >= s.S + s.R);
+                const bool rows_shared = KIND == HSTU_KIND_MFALCON ||
+                                         (KIND != HSTU_KIND_CAUSAL && KIND != HSTU_KIND_WINDOW && r0 >= s.S + s.R);
                 // real-time / history rows against non-candidate keys: the mask is j <= i (a
                 // static key precedes every real-time row)
+                // window rows: the mask depends on j - i alone unless the block's keys are part
+                // sinks, part not
                 const bool causal_rows = KIND == HSTU_KIND_CAUSAL ||
-                                         (KIND != HSTU_KIND_MFALCON && r0 >= s.S && r_hi < s.S + s.R &&
-                                          n0 < s.S + s.R);
+                                         (KIND == HSTU_KIND_WINDOW
+                                              ? n0 >= s.S || n0 + 63 < s.S
+                                              : KIND != HSTU_KIND_MFALCON && r0 >= s.S && r_hi < s.S + s.R &&
+                                                    n0 < s.S + s.R);
                 // keys n0 + k with k >= jlim are masked for every row of the block: static rows
                 // against a key block that crosses the end of the static segment, real-time rows
                 // against one that crosses the end of the history
@@ -527,6 +552,12 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     } else if (causal_rows && n0 + 63 >= s.S + s.R) {
                         jlim = s.S + s.R - n0;
                     }
+                }
+                // window rows far past a key block that crosses the end of the sinks see its
+                // sinks only (i - j >= R for the rest, and every row is past every key)
+                if (KIND == HSTU_KIND_WINDOW && wcls == 1 && !causal_rows && r0 - (n0 + 63) >= s.R) {
+                    jlim = s.S - n0;
+                    wcls = 2;
                 }
                 // MTGR candidate rows against history keys: the timestamp filter passes every
                 // pair when the rows' earliest time is after the keys' latest, and no pair when
@@ -562,7 +593,8 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const int d0 = n0 - r0 - 31;
                             for (int k = lane; k < 95; k += 32) {
                                 const int dl = d0 + k;
-                                const bool masked = causal_rows && dl > 0;
+                                const bool masked = (causal_rows && dl > 0) ||
+                                                    (KIND == HSTU_KIND_WINDOW && wcls == 1 && n0 >= s.S && -dl >= s.R);
                                 const int pi = pm == kPosUniform ? pidx_u : min(max(dl, -(p.P - 1)), p.P - 1) + p.P - 1;
                                 w_diag[k] = masked ? kMaskedHalfBias : 0.5f * s_rp[pi] + tadd;
                             }
@@ -633,7 +665,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     else if (pm >= 0 && tm == kTimeTwo)
                         fwd_block2<kBiasRowTwo>(sa, dg, cr, a_i, c0, s_rth, nbm1, pk, tc.thr, s_rth[tc.tb_lo], s_rth[tc.tb_hi]);
                     else fwd_block2<kBiasRowTime>(sa, dg, cr, a_i, c0, s_rth, nbm1, pk);
-                    if ((KIND == HSTU_KIND_MTGR || KIND == HSTU_KIND_MFSEQ) && pm >= 0 && jlim - 32 * cc < 32) {
+                    if ((KIND == HSTU_KIND_MTGR || KIND == HSTU_KIND_MFSEQ || KIND == HSTU_KIND_WINDOW) && pm >= 0 && jlim - 32 * cc < 32) {
                         // keys past the block's column limit: P = 0 (bf16 pairs, key 2e in the low half)
                         const int lim = jlim - 32 * cc;
 #pragma unroll
@@ -768,6 +800,8 @@ cudaError_t launch_attn_fwd_tc(int kind, int d, const CUtensorMap& tq, const CUt
     HSTU_FWD_CASE(HSTU_KIND_MFALCON, 64)
     HSTU_FWD_CASE(HSTU_KIND_MFSEQ, 128)
     HSTU_FWD_CASE(HSTU_KIND_MFSEQ, 64)
+    HSTU_FWD_CASE(HSTU_KIND_WINDOW, 128)
+    HSTU_FWD_CASE(HSTU_KIND_WINDOW, 64)
 #undef HSTU_FWD_CASE
     return cudaErrorInvalidValue;
 }
@@ -783,6 +817,8 @@ int attn_fwd_tc_ctas_per_sm(int kind, int d) {
     HSTU_OCC_CASE(HSTU_KIND_MFALCON, 64)
     HSTU_OCC_CASE(HSTU_KIND_MFSEQ, 128)
     HSTU_OCC_CASE(HSTU_KIND_MFSEQ, 64)
+    HSTU_OCC_CASE(HSTU_KIND_WINDOW, 128)
+    HSTU_OCC_CASE(HSTU_KIND_WINDOW, 64)
 #undef HSTU_OCC_CASE
     return 1;
 }

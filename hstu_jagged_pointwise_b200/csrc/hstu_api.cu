@@ -21,7 +21,7 @@ namespace {
 struct DevInfo {
     bool ready = false;
     int sms = 0;
-    int occ[4][2] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};   // [kind][d == 128]
+    int occ[5][2] = {};   // [kind][d == 128]
 };
 std::mutex g_mu;
 DevInfo g_dev[64];
@@ -34,7 +34,7 @@ const DevInfo* dev_info() {
     if (!d.ready) {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return nullptr;
-        for (int k = 0; k < 4; k++) {
+        for (int k = 0; k < 5; k++) {
             d.occ[k][0] = attn_fwd_tc_ctas_per_sm(k, 64);
             d.occ[k][1] = attn_fwd_tc_ctas_per_sm(k, 128);
         }
@@ -169,6 +169,11 @@ int check_mask(const hstu_mask_spec* m, int* kind) {
     if (m->kind == HSTU_MASK_MFALCON_SEQ) {
         if (!aligned(m->n_realtime, 4)) return HSTU_ERR_INVALID_ARG;
         *kind = HSTU_KIND_MFSEQ;
+        return HSTU_OK;
+    }
+    if (m->kind == HSTU_MASK_WINDOW) {
+        if (!aligned(m->n_static, 4) || !aligned(m->n_realtime, 4)) return HSTU_ERR_INVALID_ARG;
+        *kind = HSTU_KIND_WINDOW;
         return HSTU_OK;
     }
     return HSTU_ERR_INVALID_ARG;
@@ -323,7 +328,8 @@ const char* hstu_status_string(int s) {
 
 size_t hstu_attn_workspace_bytes(const hstu_dims* dims, int32_t mask_kind, int32_t is_bwd) {
     if (check_dims(dims) != HSTU_OK) return 0;
-    if (mask_kind != HSTU_MASK_CAUSAL && mask_kind != HSTU_MASK_MTGR && mask_kind != HSTU_MASK_MFALCON_SEQ)
+    if (mask_kind != HSTU_MASK_CAUSAL && mask_kind != HSTU_MASK_MTGR && mask_kind != HSTU_MASK_MFALCON_SEQ &&
+        mask_kind != HSTU_MASK_WINDOW)
         return 0;
     if (is_bwd && mask_kind == HSTU_MASK_MFALCON_SEQ) return 0;
     return attn_layout(*dims, is_bwd ? 1 : 0).total;
@@ -530,12 +536,15 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
 
     // 2. LayerNorm backward: dY (into the workspace), dU, dgamma, dbeta; or, from dL/dY,
     //    only the scaled copy of dY the tensor-core backward reads
-    // the tensor-core backward takes dY / (2 alpha): its elementwise step then needs no scaling
-    const float dy_scale = d.dtype == HSTU_F32 ? 1.0f : 0.5f / d.alpha;
+    // the tensor-core backward takes dY / (2 alpha): its elementwise step then needs no scaling.
+    // The window kind takes dY itself and scales in fp32, so that a bf16 dY is not rounded again
+    // before it enters the bias gradients.
+    const bool dy_as_is = d.dtype == HSTU_F32 || kind == HSTU_KIND_WINDOW;
+    const float dy_scale = dy_as_is ? 1.0f : 0.5f / d.alpha;
     const void* dy_ws = at<void>(workspace, L.dy);
     if (from_dy) {
-        if (d.dtype == HSTU_F32) {
-            dy_ws = dy_in;                        // the CUDA-core backward reads dY as it is
+        if (dy_as_is) {
+            dy_ws = dy_in;
         } else {
             st = cuda_status(launch_scale_bf16(static_cast<const __nv_bfloat16*>(dy_in),
                                                at<__nv_bfloat16>(workspace, L.dy), dy_scale,
@@ -617,6 +626,7 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
     bp.P = d.n_pos;
     bp.nb = d.n_tbuckets;
     bp.ld = D;
+    bp.inv_alpha = 1.0f / d.alpha;
     st = cuda_status(launch_attn_bwd_tc(kind, d.d_qk, tq, tk, tv, tdy, tdq, bp, grid, s));
     if (st != HSTU_OK) return st;
     st = cuda_status(launch_rab_reduce(rab_part, grid, d.n_pos, d.n_tbuckets, d_rab_pos, d_rab_time, s));
@@ -794,14 +804,17 @@ int hstu_debug_indices(int32_t B, int32_t mask_kind, const int32_t* seq_offsets,
                        uint8_t* mask_bits, int16_t* pos_idx, int8_t* time_bucket, void* stream) {
     if (B < 0 || n_pos < 1 || n_pos > 16384 || n_tbuckets < 1 || n_tbuckets > 64)
         return HSTU_ERR_INVALID_ARG;
-    if (mask_kind != HSTU_MASK_CAUSAL && mask_kind != HSTU_MASK_MTGR && mask_kind != HSTU_MASK_MFALCON_SEQ)
+    if (mask_kind != HSTU_MASK_CAUSAL && mask_kind != HSTU_MASK_MTGR && mask_kind != HSTU_MASK_MFALCON_SEQ &&
+        mask_kind != HSTU_MASK_WINDOW)
         return HSTU_ERR_INVALID_ARG;
     if (B == 0) return HSTU_OK;
     if (!seq_offsets || !timestamps || !pair_offsets || !mask_bits || !pos_idx || !time_bucket)
         return HSTU_ERR_INVALID_ARG;
-    if (mask_kind == HSTU_MASK_MTGR && (!n_static || !n_realtime)) return HSTU_ERR_INVALID_ARG;
+    if ((mask_kind == HSTU_MASK_MTGR || mask_kind == HSTU_MASK_WINDOW) && (!n_static || !n_realtime))
+        return HSTU_ERR_INVALID_ARG;
     if (mask_kind == HSTU_MASK_MFALCON_SEQ && !n_realtime) return HSTU_ERR_INVALID_ARG;
     const int kind = mask_kind == HSTU_MASK_MTGR ? HSTU_KIND_MTGR
+                   : mask_kind == HSTU_MASK_WINDOW ? HSTU_KIND_WINDOW
                    : (mask_kind == HSTU_MASK_MFALCON_SEQ ? HSTU_KIND_MFSEQ : HSTU_KIND_CAUSAL);
     return cuda_status(launch_debug_indices(B, kind, seq_offsets, timestamps, n_static, n_realtime,
                                             n_pos, n_tbuckets, pair_offsets, 0, mask_bits, pos_idx,

@@ -13,6 +13,8 @@
 //   Full-sequence M-FALCON (HSTU blog, section 4.2): [history ; candidates] in
 //   one row, history causal, every candidate sees all history and itself (no
 //   timestamp filter); it is the MTGR layout with no static part.
+//   Window with sinks: token i sees token j <= i when i - j < R (the window) or
+//   j < S (the first S tokens of the row, the sinks); positions are indices.
 #pragma once
 #include <stdint.h>
 
@@ -20,13 +22,15 @@
 #define HSTU_KIND_MTGR 1
 #define HSTU_KIND_MFALCON 2
 #define HSTU_KIND_MFSEQ 3
+#define HSTU_KIND_WINDOW 4
 
 namespace hstu {
 
 // Segment sizes of row b: S static tokens, R real-time / history tokens, the rest candidates.
+// Window rows: S sinks and a window of R tokens (neither is bounded by the row's length).
 __device__ __forceinline__ void segment_sizes(int kind, const int32_t* n_static, const int32_t* n_rt, int b,
                                               int L, int* S, int* R) {
-    if (kind == HSTU_KIND_MTGR) {
+    if (kind == HSTU_KIND_MTGR || kind == HSTU_KIND_WINDOW) {
         *S = n_static[b];
         *R = n_rt[b];
     } else if (kind == HSTU_KIND_MFSEQ) {
@@ -70,10 +74,11 @@ __device__ __forceinline__ int time_bucket(int64_t ti, int64_t tj, int nb) {
     return time_bucket_of_delta(abs_diff_u64(ti, tj), nb);
 }
 
-// Mask of causal, MTGR and full-sequence M-FALCON rows (i, j local to the sequence).
+// Mask of causal, window, MTGR and full-sequence M-FALCON rows (i, j local to the sequence).
 __device__ __forceinline__ bool visible(int kind, int i, int j, int S, int R, int64_t ts_i,
                                         int64_t ts_j) {
     if (kind == HSTU_KIND_CAUSAL) return j <= i;
+    if (kind == HSTU_KIND_WINDOW) return j <= i && (i - j < R || j < S);
     int ci = token_class(i, S, R), cj = token_class(j, S, R);
     if (ci == 0) return cj == 0;
     if (ci == 1) return cj == 0 || (cj == 1 && j <= i);
@@ -92,6 +97,11 @@ __device__ __forceinline__ int tile_class(int kind, int qa, int qb, int ka, int 
         return (kb <= qa) ? 2 : 1;
     }
     if (kind == HSTU_KIND_MFALCON) return 2;
+    if (kind == HSTU_KIND_WINDOW) {
+        if (ka > qb) return 0;
+        if (ka >= S && max(qa - kb, 0) >= R) return 0;          // past the sinks, before every row's window
+        return kb <= qa && (kb < S || qb - ka < R) ? 2 : 1;
+    }
     const int H = S + R;
     bool any = false;
     // static rows see static columns

@@ -98,6 +98,7 @@ struct BwdParams {
     __nv_bfloat16* dv;
     float* rab_part;          // [grid][2P-1 + nb] per-CTA rab gradient partial sums, zeroed
     int H, P, nb, ld;
+    float inv_alpha;          // 1 / alpha (window kind, which reads dY unscaled)
     DebugWait dbg;
 };
 

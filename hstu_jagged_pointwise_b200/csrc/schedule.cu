@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
             segment_sizes(p.kind, p.n_static, p.n_rt, b, Lq, &S, &R);
             if (S < 0 || R < 0 || (long long)S + R > Lq) bad = 1;
         }
+        if (p.kind == HSTU_KIND_WINDOW && (p.n_static[b] < 0 || p.n_rt[b] < 0)) bad = 1;
     }
     if (__syncthreads_or(bad)) {
         if (tid == 0) {

@@ -59,6 +59,12 @@ def make_mask(kind: str = "causal", n_static: Optional[torch.Tensor] = None,
         _need(n_realtime, "n_realtime", torch.int32)
         return capi.HstuMaskSpec(kind=capi.HSTU_MASK_MFALCON_SEQ, n_static=None,
                                  n_realtime=n_realtime.data_ptr())
+    if kind == "window":
+        # row b: the first n_static[b] tokens (sinks) and the last n_realtime[b] tokens up to itself (window)
+        _need(n_static, "n_static", torch.int32)
+        _need(n_realtime, "n_realtime", torch.int32)
+        return capi.HstuMaskSpec(kind=capi.HSTU_MASK_WINDOW, n_static=n_static.data_ptr(),
+                                 n_realtime=n_realtime.data_ptr())
     raise ValueError(f"unknown mask kind {kind!r}")
 
 
@@ -444,7 +450,7 @@ def debug_indices(seq_offsets, timestamps, mask_kind: str = "causal", n_static=N
     pi = torch.zeros(n, dtype=torch.int16, device=seq_offsets.device)
     tb = torch.zeros(n, dtype=torch.int8, device=seq_offsets.device)
     kind = {"causal": capi.HSTU_MASK_CAUSAL, "mtgr": capi.HSTU_MASK_MTGR,
-            "mfalcon_seq": capi.HSTU_MASK_MFALCON_SEQ}[mask_kind]
+            "mfalcon_seq": capi.HSTU_MASK_MFALCON_SEQ, "window": capi.HSTU_MASK_WINDOW}[mask_kind]
     st = capi.LIB.hstu_debug_indices(L.numel(), kind, _p(seq_offsets), _p(timestamps), _p(n_static),
                                      _p(n_realtime), n_pos, n_tbuckets, _p(po), _p(m), _p(pi), _p(tb), _stream())
     capi.check(st, "hstu_debug_indices")

@@ -43,7 +43,7 @@ MASK_MTGR = 1
 class Workload:
     """One batch of synthetic inputs (torch CPU tensors / numpy arrays)."""
     name: str
-    kind: str                      # "causal" | "mtgr" | "mfalcon" | "mfalcon_seq"
+    kind: str                      # "causal" | "mtgr" | "mfalcon" | "mfalcon_seq" | "window"
     dtype: torch.dtype             # element type of q/k/v/u (bf16 or fp32)
     H: int
     d: int
@@ -62,8 +62,8 @@ class Workload:
     k: Optional[torch.Tensor] = None
     v: Optional[torch.Tensor] = None
     u: Optional[torch.Tensor] = None
-    n_static: Optional[np.ndarray] = None     # int32 [B] (mtgr)
-    n_realtime: Optional[np.ndarray] = None   # int32 [B] (mtgr; history length for mfalcon_seq)
+    n_static: Optional[np.ndarray] = None     # int32 [B] (mtgr; sinks for window)
+    n_realtime: Optional[np.ndarray] = None   # int32 [B] (mtgr; history length for mfalcon_seq; window for window)
     grad: Optional[torch.Tensor] = None       # upstream gradient of o_pre [T, H*d]
     # M-FALCON layout
     hist_offsets: Optional[np.ndarray] = None
@@ -217,6 +217,15 @@ def make_causal(lengths, H: int, d: int, dtype=torch.bfloat16, seed: int = 0,
     return Workload(name=name, kind="causal", dtype=dtype, H=H, d=d, alpha=float(alpha),
                     rab_pos=rp, rab_time=rt, gamma=g, beta=b, offsets=offsets, ts=ts,
                     q=q, k=k, v=v, u=u, grad=grad)
+
+
+def make_window(lengths, sinks, windows, H: int, d: int, dtype=torch.bfloat16, seed: int = 0, **kw) -> Workload:
+    """Causal rows under a sliding window with sinks: row b sees its last windows[b] tokens and
+    its first sinks[b]."""
+    w = make_causal(lengths, H, d, dtype, seed, name=kw.pop("name", "window"), **kw)
+    w.kind = "window"
+    w.n_static, w.n_realtime = np.asarray(sinks, np.int32), np.asarray(windows, np.int32)
+    return w
 
 
 def mtgr_user(rng, n_profile: int, n_long: int, n_rt: int, n_cand: int, start: int = T0):

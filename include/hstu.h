@@ -26,6 +26,10 @@
  * one pass scores the candidates against a causal history): history tokens are
  * causal, a candidate sees every history token and itself, and all candidates
  * sit at pos = R.  It is forward only (a scoring pass).
+ * HSTU_MASK_WINDOW is a causal sliding window with sinks: token i of row b sees
+ * token j <= i when i - j < W_b (the last W_b tokens up to and with itself) or
+ * j < S_b (the row's first S_b tokens, which stay visible).  W_b = S_b = 0 leaves
+ * a row nothing to see: Y = 0 there.  Forward and backward.
  *
  * Conventions shared by every entry point:
  *  - Tensor pointers are DEVICE pointers owned by the caller.  Host structs
@@ -79,13 +83,18 @@ typedef enum {
 
 typedef enum { HSTU_BF16 = 0, HSTU_F32 = 1 } hstu_dtype;
 
-typedef enum { HSTU_MASK_CAUSAL = 0, HSTU_MASK_MTGR = 1, HSTU_MASK_MFALCON_SEQ = 2 } hstu_mask_kind;
+typedef enum { HSTU_MASK_CAUSAL = 0, HSTU_MASK_MTGR = 1, HSTU_MASK_MFALCON_SEQ = 2, HSTU_MASK_WINDOW = 3 } hstu_mask_kind;
 
 /* Mask description.  For HSTU_MASK_MTGR, n_static[b] (profile + long-term
  * tokens, seen bidirectionally) and n_realtime[b] are DEVICE int32 [B]; the
  * remaining L_b - n_static[b] - n_realtime[b] tokens of row b are candidates.
  * For HSTU_MASK_MFALCON_SEQ, n_realtime[b] is the history length of row b (the
- * rest are candidates) and n_static is ignored (may be NULL).  Both pointers
+ * rest are candidates) and n_static is ignored (may be NULL).
+ * For HSTU_MASK_WINDOW, n_static[b] is the number of sinks S_b and n_realtime[b]
+ * the window W_b of row b, each >= 0 and either may exceed the row's length (a
+ * negative one sets the device status word like a bad segment size).  A row's
+ * keys and values must be finite: a masked NaN or infinity inside a 128-token
+ * tile that the row sees part of reaches its sum, as with the other masks.  Both pointers
  * are ignored for HSTU_MASK_CAUSAL.  Segment sizes outside [0, L_b] set the
  * device status word (HSTU_ERR_DEVICE_BOUNDS) and the launch writes nothing. */
 typedef struct {

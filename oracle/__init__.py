@@ -28,6 +28,7 @@ _lib = None
 MASK_CAUSAL = 0
 MASK_MTGR = 1
 MASK_MFSEQ = 2   # full-sequence M-FALCON: [history ; candidates], n_realtime = history length
+MASK_WINDOW = 3  # sliding window: n_static = sinks, n_realtime = window
 
 
 def build(force: bool = False) -> str:
@@ -119,11 +120,11 @@ def _ptr(a):
 
 
 def _kind(w) -> int:
-    return {"mtgr": MASK_MTGR, "mfalcon_seq": MASK_MFSEQ}.get(w.kind, MASK_CAUSAL)
+    return {"mtgr": MASK_MTGR, "mfalcon_seq": MASK_MFSEQ, "window": MASK_WINDOW}.get(w.kind, MASK_CAUSAL)
 
 
 def _segs(w):
-    if w.kind == "mtgr":
+    if w.kind in ("mtgr", "window"):
         return _c(w.n_static, np.int32), _c(w.n_realtime, np.int32)
     if w.kind == "mfalcon_seq":
         return np.zeros(len(w.n_realtime), np.int32), _c(w.n_realtime, np.int32)

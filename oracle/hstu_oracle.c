@@ -24,6 +24,8 @@
  *       [history ; candidates] before caching): history tokens causal among
  *       themselves, each candidate sees every history token and itself; no
  *       timestamp filter.
+ *     Window with sinks: a token sees the last R tokens up to itself and the
+ *       first S tokens of its row.
  *
  * Readings where the pages are silent (each also listed with the design notes):
  *   - alpha divides A after SiLU (Y = sum_j mask*SiLU(z)*v / alpha); no 1/sqrt(d).
@@ -49,6 +51,7 @@
 #define ORACLE_CAUSAL 0
 #define ORACLE_MTGR 1
 #define ORACLE_MFSEQ 2      /* full-sequence M-FALCON: n_rt[b] = history length, no static part */
+#define ORACLE_WINDOW 3     /* sliding window: n_static[b] = sinks, n_rt[b] = window */
 
 /* ------------------------------------------------------------------ */
 /* index rules                                                         */
@@ -93,6 +96,7 @@ static int time_bucket(int64_t ti, int64_t tj, int nb) {
 /* ts points at the first token of the sequence */
 static int visible(int kind, int64_t i, int64_t j, int64_t S, int64_t R, const int64_t* ts) {
     if (kind == ORACLE_CAUSAL) return j <= i;
+    if (kind == ORACLE_WINDOW) return j <= i && (j < S || j > i - R);
     int ci = token_class(i, S, R), cj = token_class(j, S, R);
     if (ci == 0) return cj == 0;
     if (ci == 1) return cj == 0 || (cj == 1 && j <= i);
@@ -143,7 +147,7 @@ static int64_t find_seq(const int32_t* off, int32_t B, int64_t t) {
 
 static void seg_sizes(int kind, const int32_t* n_static, const int32_t* n_rt, int64_t b, int64_t L,
                       int64_t* S, int64_t* R) {
-    if (kind == ORACLE_MTGR) {
+    if (kind == ORACLE_MTGR || kind == ORACLE_WINDOW) {
         *S = n_static[b];
         *R = n_rt[b];
     } else if (kind == ORACLE_MFSEQ) {

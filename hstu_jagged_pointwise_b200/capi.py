@@ -1,6 +1,7 @@
-"""ctypes declarations of libhstu_b200 (the C ABI in include/hstu.h).
+"""ctypes declarations of libhstu_b200 (the C ABI in include/hstu.h) and of
+libhstu_cache_b200 (include/hstu_cache.h).
 
-Importing this module loads the in-tree shared library and raises when it is
+Importing this module loads the in-tree shared libraries and raises when one is
 missing: there is no CPU fallback for any entry point.
 """
 from __future__ import annotations
@@ -10,6 +11,7 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libhstu_b200.so")
+CACHE_LIB_PATH = os.path.join(HERE, "libhstu_cache_b200.so")
 
 HSTU_OK = 0
 HSTU_ERR_INVALID_ARG = -1
@@ -18,6 +20,7 @@ HSTU_ERR_CUDA = -3
 HSTU_ERR_DEVICE_TIMEOUT = -4
 HSTU_ERR_DEVICE_BOUNDS = -5
 HSTU_ERR_WORKSPACE = -6
+HSTU_ERR_CACHE_FULL = -7
 
 HSTU_BF16 = 0
 HSTU_F32 = 1
@@ -35,6 +38,13 @@ EXPORTS = (
     "hstu_attn_workspace_bytes_gln", "hstu_f1_fwd", "hstu_f2_fwd", "hstu_f1_bwd_workspace_bytes",
     "hstu_f2_bwd_workspace_bytes", "hstu_f1_bwd", "hstu_f2_bwd", "hstu_sl_sample", "hstu_gather_rows",
     "hstu_pack_balanced", "hstu_debug_set_wait_fault", "hstu_attn_bwd_dy",
+)
+
+# every symbol include/hstu_cache.h declares
+CACHE_EXPORTS = (
+    "hstu_cache_workspace_bytes", "hstu_cache_append", "hstu_cache_fork", "hstu_cache_compact", "hstu_cache_free",
+    "hstu_tree_workspace_bytes", "hstu_tree_score", "hstu_cache_check_device_error",
+    "hstu_cache_debug_set_wait_fault",
 )
 
 NOALLOC_SCRATCH_BYTES = 4 << 20   # HSTU_NOALLOC_SCRATCH_BYTES
@@ -60,6 +70,17 @@ class HstuMfalconDims(C.Structure):
                 ("d_qk", C.c_int32), ("d_v", C.c_int32), ("dtype", C.c_int32), ("n_pos", C.c_int32),
                 ("n_tbuckets", C.c_int32), ("max_hist_len", C.c_int32), ("max_cand_len", C.c_int32),
                 ("alpha", C.c_float), ("ln_eps", C.c_float)]
+
+
+class HstuPageCache(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("page_size", C.c_int32), ("n_slots", C.c_int32), ("max_pages", C.c_int32),
+                ("row_elems", C.c_int32), ("dtype", C.c_int32), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("ts", C.c_void_p), ("page_table", C.c_void_p), ("lens", C.c_void_p), ("ref", C.c_void_p)]
+
+
+class HstuTreeDims(C.Structure):
+    _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("H", C.c_int32), ("d", C.c_int32), ("n_pos", C.c_int32),
+                ("n_tbuckets", C.c_int32), ("max_nodes", C.c_int32), ("alpha", C.c_float), ("ln_eps", C.c_float)]
 
 
 class HstuError(RuntimeError):
@@ -137,7 +158,31 @@ def load():
     return lib
 
 
+def load_cache():
+    if not os.path.exists(CACHE_LIB_PATH):
+        raise ImportError(
+            f"{CACHE_LIB_PATH} is missing: build it with `python -m hstu_jagged_pointwise_b200.build` "
+            "(there is no CPU fallback)")
+    lib = C.CDLL(CACHE_LIB_PATH)
+    P, S, i32 = C.c_void_p, C.c_size_t, C.c_int32
+    PC, TD = C.POINTER(HstuPageCache), C.POINTER(HstuTreeDims)
+    for name, args, res in (
+            ("hstu_cache_workspace_bytes", [PC], S),
+            ("hstu_cache_append", [PC, i32, P, P, i32, P, i32, P, P, P, P, S, P], C.c_int),
+            ("hstu_cache_fork", [PC, i32, P, P, P, S, P], C.c_int),
+            ("hstu_cache_compact", [PC, i32, P, P, i32, P, P, S, P], C.c_int),
+            ("hstu_cache_free", [PC, i32, P, P, S, P], C.c_int),
+            ("hstu_tree_workspace_bytes", [TD, PC], S),
+            ("hstu_tree_score", [TD, PC] + [P] * 17 + [S, P], C.c_int),
+            ("hstu_cache_check_device_error", [P, P], C.c_int),
+            ("hstu_cache_debug_set_wait_fault", [C.c_int64, i32], C.c_int)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, res
+    return lib
+
+
 LIB = load()
+CACHE = load_cache()
 
 
 def status_string(status: int) -> str:
@@ -171,10 +216,13 @@ class wait_fault:
 
     def __enter__(self):
         check(LIB.hstu_debug_set_wait_fault(self.limit, 1 if self.withhold else 0), "hstu_debug_set_wait_fault")
+        check(CACHE.hstu_cache_debug_set_wait_fault(self.limit, 1 if self.withhold else 0),
+              "hstu_cache_debug_set_wait_fault")
         return self
 
     def __exit__(self, *exc):
         check(LIB.hstu_debug_set_wait_fault(0, 0), "hstu_debug_set_wait_fault")
+        check(CACHE.hstu_cache_debug_set_wait_fault(0, 0), "hstu_cache_debug_set_wait_fault")
         return False
 
 

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/hstu.h"
+#include "host_util.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -80,39 +81,6 @@ cudaError_t ensure_smem_limit(const void* fn, int bytes) {
 namespace {
 
 // ------------------------------------------------------------------ TMA descriptors
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// [rows, cols] bf16 row-major; box = 64 columns (128 B, one swizzle row) x box_rows rows.
-bool make_tmap(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows = 128) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 // [rows, cols] fp32 row-major, no swizzle; box = box_cols x box_rows (box_cols * 4 B a multiple of 16).
 bool make_tmap_f32(CUtensorMap* m, void* base, long long rows, long long cols, int box_cols, int box_rows) {
     EncodeTiledFn fn = encode_fn();
@@ -128,8 +96,6 @@ bool make_tmap_f32(CUtensorMap* m, void* base, long long rows, long long cols, i
 }
 
 // ------------------------------------------------------------------ checks
-bool aligned(const void* p, size_t a) { return p && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int elem_size(int dtype) { return dtype == HSTU_F32 ? 4 : 2; }
 
 bool d_supported(int dtype, int d) {
@@ -239,12 +205,6 @@ T* at(void* ws, size_t off) {
     return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
-int cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return HSTU_OK;
-    fprintf(stderr, "libhstu_b200: CUDA error %s\n", cudaGetErrorString(e));
-    return HSTU_ERR_CUDA;
-}
-
 SimtParams simt_params(const hstu_dims& d, int kind, const hstu_mask_spec& m, const int32_t* off,
                        const int64_t* ts, const float* rp, const float* rt, const void* q,
                        const void* k, const void* v, const Control* ctrl) {
@@ -322,6 +282,7 @@ const char* hstu_status_string(int s) {
         case HSTU_ERR_DEVICE_TIMEOUT: return "a bounded device wait timed out";
         case HSTU_ERR_DEVICE_BOUNDS: return "offsets, lengths or segment sizes are invalid";
         case HSTU_ERR_WORKSPACE: return "workspace missing or too small";
+        case HSTU_ERR_CACHE_FULL: return "the page pool has too few free pages";
         default: return "unknown status";
     }
 }

@@ -437,6 +437,178 @@ def mfalcon_cache_history(seq_offsets, timestamps, n_history, k, v, hist_rows: O
     return out
 
 
+# ----------------------------------------------------------------------------
+# the paged history cache and the tree scorer that reads it (include/hstu_cache.h)
+# ----------------------------------------------------------------------------
+
+def _on(t, name: str, device, dtype):
+    _need(t, name, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+class PagedCache:
+    """User histories in pages of a common pool.
+
+    Slot s holds ``lens[s]`` rows; row r is row ``r % page_size`` of page
+    ``page_table[s, r // page_size]`` of ``k``, ``v`` [n_pages, page_size, row_elems] and ``ts``
+    [n_pages, page_size].  ``ref[p]`` counts the slots that hold page p (0: free).  The tensors are
+    the cache itself: read them freely, and change them only through the methods, or as a whole.
+
+    The methods are asynchronous on the current stream and change the tables in place; calls on
+    one cache must be ordered (one stream, or events).  What the device refuses (a slot named
+    twice or out of range, offsets that do not fit, too few free pages) changes nothing and is
+    reported by check_device_error()."""
+
+    def __init__(self, n_pages: int, page_size: int, n_slots: int, max_pages: int, row_elems: int,
+                 dtype: torch.dtype = torch.bfloat16, device="cuda"):
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype must be one of {sorted(map(str, _DTYPES))}, got {dtype}")
+        z = lambda *shape, dt=torch.int32: torch.zeros(*shape, dtype=dt, device=device)
+        self.k = z(n_pages, page_size, row_elems, dt=dtype)
+        self.v = z(n_pages, page_size, row_elems, dt=dtype)
+        self.ts = z(n_pages, page_size, dt=torch.int64)
+        self.page_table = torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=device)
+        self.lens, self.ref = z(n_slots), z(n_pages)
+        self.device, self.dtype, self.row_elems = self.k.device, dtype, row_elems
+        if self.device.type != "cuda":
+            raise ValueError("a PagedCache lives on a CUDA device (no CPU path exists)")
+        self.desc = capi.HstuPageCache(
+            n_pages=n_pages, page_size=page_size, n_slots=n_slots, max_pages=max_pages, row_elems=row_elems,
+            dtype=_DTYPES[dtype], k=self.k.data_ptr(), v=self.v.data_ptr(), ts=self.ts.data_ptr(),
+            page_table=self.page_table.data_ptr(), lens=self.lens.data_ptr(), ref=self.ref.data_ptr())
+        n = capi.CACHE.hstu_cache_workspace_bytes(C.byref(self.desc))
+        if n == 0:
+            raise capi.HstuError(capi.HSTU_ERR_INVALID_ARG, "hstu_cache_workspace_bytes")
+        self.ws = workspace(int(n), self.device)
+
+    def _call(self, fn, *args):
+        with torch.cuda.device(self.device):
+            st = getattr(capi.CACHE, fn)(C.byref(self.desc), *args, _p(self.ws), self.ws.numel(), _stream())
+        capi.check(st, fn)
+
+    def append(self, slots, row_offsets, k, v, ts, rows: Optional[torch.Tensor] = None) -> None:
+        """Appends rows row_offsets[i] .. row_offsets[i+1]-1 to slots[i].  Row r is row r of k, v
+        [n, row_elems] and ts [n], or row rows[r] (int32).  A shared, partly filled last page is
+        copied first, so that its other holders keep theirs."""
+        _on(slots, "slots", self.device, torch.int32)
+        _on(row_offsets, "row_offsets", self.device, torch.int32)
+        for t, n in ((k, "k"), (v, "v")):
+            _on(t, n, self.device, self.dtype)
+            if t.dim() != 2 or t.shape[1] != self.row_elems:
+                raise ValueError(f"{n} must be [n, {self.row_elems}]")
+        _on(ts, "ts", self.device, torch.int64)
+        if v.shape[0] != k.shape[0] or ts.numel() != k.shape[0]:
+            raise ValueError("k, v and ts must have the same number of rows")
+        if row_offsets.numel() != slots.numel() + 1:
+            raise ValueError("row_offsets must have one entry more than slots")
+        if rows is not None:
+            _on(rows, "rows", self.device, torch.int32)
+        T = k.shape[0] if rows is None else rows.numel()
+        self._call("hstu_cache_append", slots.numel(), _p(slots), _p(row_offsets), T, _p(rows), k.shape[0], _p(k), _p(v),
+                   _p(ts))
+
+    def fork(self, src, dst) -> None:
+        """The empty slots dst[i] come to hold the rows of src[i]; the pages are shared."""
+        _on(src, "src", self.device, torch.int32)
+        _on(dst, "dst", self.device, torch.int32)
+        if src.numel() != dst.numel():
+            raise ValueError("src and dst must have the same number of slots")
+        self._call("hstu_cache_fork", dst.numel(), _p(src), _p(dst))
+
+    def compact(self, slots, keep_offsets, keep_rows) -> None:
+        """slots[i] keeps its rows keep_rows[keep_offsets[i]] .. keep_rows[keep_offsets[i+1]-1], in
+        that order, in fresh pages; its old pages are released."""
+        _on(slots, "slots", self.device, torch.int32)
+        _on(keep_offsets, "keep_offsets", self.device, torch.int32)
+        _on(keep_rows, "keep_rows", self.device, torch.int32)
+        if keep_offsets.numel() != slots.numel() + 1:
+            raise ValueError("keep_offsets must have one entry more than slots")
+        self._call("hstu_cache_compact", slots.numel(), _p(slots), _p(keep_offsets), keep_rows.numel(), _p(keep_rows))
+
+    def free(self, slots) -> None:
+        """Empties the slots and releases their pages."""
+        _on(slots, "slots", self.device, torch.int32)
+        self._call("hstu_cache_free", slots.numel(), _p(slots))
+
+    def check_device_error(self) -> int:
+        with torch.cuda.device(self.device):
+            return int(capi.CACHE.hstu_cache_check_device_error(_p(self.ws), _stream()))
+
+
+class TreeScorer:
+    """Trees of candidates over the histories of a PagedCache (hstu_tree_score).
+
+    Tree b holds nodes node_offsets[b] .. node_offsets[b+1]-1 and reads slot slots[b].  parent
+    (int32 [T]) is each node's parent within its tree, a smaller index, or -1.  A node sees the
+    history, its ancestors and itself; with n_sink and window (int32 [B]) only positions that the
+    window mask would let it see.  One-node trees are M-FALCON candidates or a next event.
+
+    Reusing a scorer keeps its workspace; the cache may grow between calls (lengths are read on
+    the device at each call).  One scorer serves one stream at a time."""
+
+    def __init__(self, cache: PagedCache, slots, node_offsets, parent, node_ts, H: int, d: int, alpha: float,
+                 max_nodes: int, n_sink: Optional[torch.Tensor] = None, window: Optional[torch.Tensor] = None,
+                 n_pos: int = 256, n_tbuckets: int = 64, ln_eps: float = 1e-5):
+        for t, n, dt in ((slots, "slots", torch.int32), (node_offsets, "node_offsets", torch.int32),
+                         (parent, "parent", torch.int32), (node_ts, "node_ts", torch.int64)):
+            _on(t, n, cache.device, dt)
+        B, T = slots.numel(), node_ts.numel()
+        if node_offsets.numel() != B + 1 or parent.numel() != T:
+            raise ValueError("node_offsets must have one entry more than slots, parent one for each node")
+        if (n_sink is None) != (window is None):
+            raise ValueError("n_sink and window go together")
+        for t, n in ((n_sink, "n_sink"), (window, "window")):
+            if t is not None:
+                _on(t, n, cache.device, torch.int32)
+                if t.numel() != B:
+                    raise ValueError(f"{n} must have one entry for each tree")
+        self.cache, self.slots, self.node_offsets, self.parent, self.node_ts = cache, slots, node_offsets, parent, node_ts
+        self.n_sink, self.window = n_sink, window
+        self.H, self.d, self.B, self.T = H, d, B, T
+        self.n_pos, self.n_tbuckets = n_pos, n_tbuckets
+        self.dims = capi.HstuTreeDims(B=B, T=T, H=H, d=d, n_pos=n_pos, n_tbuckets=n_tbuckets, max_nodes=max_nodes,
+                                      alpha=float(alpha), ln_eps=float(ln_eps))
+        n = capi.CACHE.hstu_tree_workspace_bytes(C.byref(self.dims), C.byref(cache.desc))
+        if n == 0:
+            raise capi.HstuError(capi.HSTU_ERR_INVALID_ARG, "hstu_tree_workspace_bytes")
+        with torch.cuda.device(cache.device):
+            self.ws = workspace(int(n), cache.device, zero=False)
+            self.ws[:256].zero_()               # the control block; the rest needs no clearing
+
+    def score(self, q, k, v, u, rab_pos, rab_time, ln_gamma, ln_beta, out: Optional[dict] = None) -> dict:
+        """y and o_pre [T, H*d] of the nodes with queries, keys, values and gates q, k, v, u."""
+        dev, D = self.cache.device, self.H * self.d
+        for t, n in ((q, "q"), (k, "k"), (v, "v"), (u, "u")):
+            _on(t, n, dev, torch.bfloat16)
+            if t.numel() != self.T * D:
+                raise ValueError(f"{n} must be [{self.T}, {D}]")
+        for t, n, size in ((rab_pos, "rab_pos", 2 * self.n_pos - 1), (rab_time, "rab_time", self.n_tbuckets),
+                           (ln_gamma, "ln_gamma", D), (ln_beta, "ln_beta", D)):
+            _on(t, n, dev, torch.float32)
+            if t.numel() != size:
+                raise ValueError(f"{n} must have {size} entries")
+        if out is None:
+            out = dict(y=torch.empty_like(q), o_pre=torch.empty_like(q))
+        else:
+            for n in ("y", "o_pre"):
+                _on(out[n], n, dev, torch.bfloat16)
+                if out[n].numel() != self.T * D:
+                    raise ValueError(f"{n} must be [{self.T}, {D}]")
+        with torch.cuda.device(dev):
+            st = capi.CACHE.hstu_tree_score(
+                C.byref(self.dims), C.byref(self.cache.desc), _p(self.slots), _p(self.node_offsets), _p(self.parent),
+                _p(self.node_ts), _p(q), _p(k), _p(v), _p(u), _p(self.n_sink), _p(self.window), _p(rab_pos),
+                _p(rab_time), _p(ln_gamma), _p(ln_beta), _p(out["y"]), _p(out["o_pre"]), _p(self.ws), self.ws.numel(),
+                _stream())
+        capi.check(st, "hstu_tree_score")
+        return out
+
+    def check_device_error(self) -> int:
+        with torch.cuda.device(self.cache.device):
+            return int(capi.CACHE.hstu_cache_check_device_error(_p(self.ws), _stream()))
+
+
 def debug_indices(seq_offsets, timestamps, mask_kind: str = "causal", n_static=None, n_realtime=None,
                   n_pos: int = 256, n_tbuckets: int = 64):
     """Per-pair (mask, rab_pos index, time bucket) from the kernels' own device functions."""

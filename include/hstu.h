@@ -78,7 +78,8 @@ typedef enum {
     HSTU_ERR_CUDA = -3,          /* a CUDA runtime call or launch failed */
     HSTU_ERR_DEVICE_TIMEOUT = -4,/* a bounded device wait ran out (device status word) */
     HSTU_ERR_DEVICE_BOUNDS = -5, /* offsets / lengths / segments invalid (device status word) */
-    HSTU_ERR_WORKSPACE = -6      /* workspace missing or smaller than the query returned */
+    HSTU_ERR_WORKSPACE = -6,     /* workspace missing or smaller than the query returned */
+    HSTU_ERR_CACHE_FULL = -7     /* a page cache has too few free pages (device status word; hstu_cache.h) */
 } hstu_status;
 
 typedef enum { HSTU_BF16 = 0, HSTU_F32 = 1 } hstu_dtype;

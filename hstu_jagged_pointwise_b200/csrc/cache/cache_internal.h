@@ -7,7 +7,6 @@
 namespace hstu {
 
 constexpr int kStatusFull = 4;       // the pool had too few free pages
-constexpr int kTreeGroup = 64;       // nodes of a tree that one work item scores together
 constexpr int kTreeMaxNodes = 8192;  // largest tree (its parents lie in shared memory)
 constexpr int kPlanThreads = 1024;
 

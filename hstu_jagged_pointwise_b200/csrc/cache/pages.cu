@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(CopyParams p) {
         } else if (!COMPACT && lane < kRowsPerWarp && r < total) {
             const int q = (int)((r - p.T) / ps), row = (int)((r - p.T) % ps);
             const int pg = p.cow[q], n = p.old_len[q];
-            if (pg >= 0 && row < n % ps) {
+            // the whole page but the rows that are written on
+            if (pg >= 0 && (row < n % ps || row - n % ps >= __ldg(p.off + q + 1) - __ldg(p.off + q))) {
                 src_mine = pg * ps + row;
                 dst_mine = p.c.page_table[(size_t)p.slots[q] * p.c.max_pages + n / ps] * ps + row;
                 pool_mine = 1;

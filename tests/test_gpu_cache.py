@@ -41,7 +41,7 @@ class Model:
         for s, p, n in freed:
             q = self.pages[s][n // self.ps]
             for t in (self.k, self.v, self.ts):
-                t[q, :n % self.ps] = t[p, :n % self.ps]
+                t[q] = t[p]
             self.ref[p] -= 1
         for i, s in enumerate(slots):
             for r in range(off[i], off[i + 1]):

@@ -465,9 +465,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         bool ok = true;
         for (int it_use = 0;; it_use++) {
             const int slot = it_use & 1;
-            int idx = 0;
-            if (lane == 0) idx = atomicAdd(&p.ctrl->counter, 1);
-            idx = __shfl_sync(kAll, idx, 0);
+            int idx = blockIdx.x;                           // the first item by position, the others by demand
+            if (it_use > 0) {
+                if (lane == 0) idx = atomicAdd(&p.ctrl->counter, 1) + gridDim.x;
+                idx = __shfl_sync(kAll, idx, 0);
+            }
             Item s;
             s.b = -1;
             int pg0 = -1, pg1 = -1;

@@ -21,12 +21,19 @@ from . import capi
 _DTYPES = {torch.bfloat16: capi.HSTU_BF16, torch.float32: capi.HSTU_F32}
 
 
+# Addresses and streams go as plain integers: the declared argument types make pointers of them.
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without building a Stream object (3 us a call) where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype=None):
@@ -442,9 +449,18 @@ def mfalcon_cache_history(seq_offsets, timestamps, n_history, k, v, hist_rows: O
 # ----------------------------------------------------------------------------
 
 def _on(t, name: str, device, dtype):
+    if t.dtype is dtype and t.device == device and t.is_contiguous():
+        return
     _need(t, name, dtype)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _on_device(device, fn, *args) -> int:
+    """fn(*args, stream) with `device` current, on its current stream."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _stream())
+    with torch.cuda.device(device):
+        return fn(*args, _stream())
 
 
 class PagedCache:
@@ -481,11 +497,10 @@ class PagedCache:
         if n == 0:
             raise capi.HstuError(capi.HSTU_ERR_INVALID_ARG, "hstu_cache_workspace_bytes")
         self.ws = workspace(int(n), self.device)
+        self._ref, self._ws = C.byref(self.desc), (self.ws.data_ptr(), self.ws.numel())
 
     def _call(self, fn, *args):
-        with torch.cuda.device(self.device):
-            st = getattr(capi.CACHE, fn)(C.byref(self.desc), *args, _p(self.ws), self.ws.numel(), _stream())
-        capi.check(st, fn)
+        capi.check(_on_device(self.device, getattr(capi.CACHE, fn), self._ref, *args, *self._ws), fn)
 
     def append(self, slots, row_offsets, k, v, ts, rows: Optional[torch.Tensor] = None) -> None:
         """Appends rows row_offsets[i] .. row_offsets[i+1]-1 to slots[i].  Row r is row r of k, v
@@ -532,8 +547,7 @@ class PagedCache:
         self._call("hstu_cache_free", slots.numel(), _p(slots))
 
     def check_device_error(self) -> int:
-        with torch.cuda.device(self.device):
-            return int(capi.CACHE.hstu_cache_check_device_error(_p(self.ws), _stream()))
+        return int(_on_device(self.device, capi.CACHE.hstu_cache_check_device_error, _p(self.ws)))
 
 
 class TreeScorer:
@@ -575,6 +589,9 @@ class TreeScorer:
         with torch.cuda.device(cache.device):
             self.ws = workspace(int(n), cache.device, zero=False)
             self.ws[:256].zero_()               # the control block; the rest needs no clearing
+        # what every call passes
+        self._head = (C.byref(self.dims), C.byref(cache.desc), _p(slots), _p(node_offsets), _p(parent), _p(node_ts))
+        self._rule, self._ws = (_p(n_sink), _p(window)), (self.ws.data_ptr(), self.ws.numel())
 
     def score(self, q, k, v, u, rab_pos, rab_time, ln_gamma, ln_beta, out: Optional[dict] = None) -> dict:
         """y and o_pre [T, H*d] of the nodes with queries, keys, values and gates q, k, v, u."""
@@ -595,18 +612,15 @@ class TreeScorer:
                 _on(out[n], n, dev, torch.bfloat16)
                 if out[n].numel() != self.T * D:
                     raise ValueError(f"{n} must be [{self.T}, {D}]")
-        with torch.cuda.device(dev):
-            st = capi.CACHE.hstu_tree_score(
-                C.byref(self.dims), C.byref(self.cache.desc), _p(self.slots), _p(self.node_offsets), _p(self.parent),
-                _p(self.node_ts), _p(q), _p(k), _p(v), _p(u), _p(self.n_sink), _p(self.window), _p(rab_pos),
-                _p(rab_time), _p(ln_gamma), _p(ln_beta), _p(out["y"]), _p(out["o_pre"]), _p(self.ws), self.ws.numel(),
-                _stream())
+        y, o = out["y"], out["o_pre"]
+        st = _on_device(dev, capi.CACHE.hstu_tree_score, *self._head, q.data_ptr(), k.data_ptr(), v.data_ptr(), u.data_ptr(),
+                        *self._rule, rab_pos.data_ptr(), rab_time.data_ptr(), ln_gamma.data_ptr(), ln_beta.data_ptr(),
+                        y.data_ptr(), o.data_ptr(), *self._ws)
         capi.check(st, "hstu_tree_score")
         return out
 
     def check_device_error(self) -> int:
-        with torch.cuda.device(self.cache.device):
-            return int(capi.CACHE.hstu_cache_check_device_error(_p(self.ws), _stream()))
+        return int(_on_device(self.cache.device, capi.CACHE.hstu_cache_check_device_error, _p(self.ws)))
 
 
 def debug_indices(seq_offsets, timestamps, mask_kind: str = "causal", n_static=None, n_realtime=None,

@@ -1,7 +1,10 @@
 // pages.cu -- page operators of the paged history cache: append, fork, compact, free.
 //
-// Each operator is a plan by one CTA, which checks every request before it changes
-// anything, and (append, compact) a copy by a grid of warps.
+// Every request is checked before anything changes.  append and compact plan in one CTA
+// (each step needs the one before it for all requests) and copy with a grid of warps;
+// fork and free, whose work is one table entry and one reference count a page, take a
+// cluster of eight CTAs, which agree through distributed shared memory: 256 forks of 36
+// pages take one SM 10 us, since its requests to L2 are that many separate sectors.
 //   append   rows n .. n + c - 1 of a slot that held n; pages needed =
 //            ceil((n + c) / ps) - ceil(n / ps), and one more where the last page has
 //            room but is shared (copied, then written: copy-on-write)
@@ -11,6 +14,8 @@
 // The k-th page needed (requests in order) is the k-th free page (ref == 0) of the
 // pool, so the result does not depend on timing.  The reference counts change by
 // integer atomics only.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "cache_internal.h"
@@ -35,7 +40,7 @@ PageWs page_ws(const hstu_page_cache& c) {
         off = align_up(off + bytes, 256);
         return at;
     };
-    w.claim = take((size_t)c.n_slots * 4);       // 1 + request that names the slot
+    w.claim = take((size_t)c.n_slots * 4);       // 1 while a request names the slot, 0 between calls
     w.base = take((size_t)c.n_slots * 4);        // request: its first place in the free list
     w.old_len = take((size_t)c.n_slots * 4);     // request: rows the slot held
     w.cow = take((size_t)c.n_slots * 4);         // request: the shared page to copy, or -1
@@ -91,24 +96,35 @@ __device__ __forceinline__ int block_exclusive(int v, int* s_warp, int* total) {
 
 __device__ __forceinline__ int pages_of(int rows, int ps) { return (rows + ps - 1) / ps; }
 
-// Names every request's slot in claim; 1 when one is out of range or named twice, or
-// its length is none the cache can hold.  claim is cleared first.
-__device__ int claim_slots(const PlanParams& p) {
-    int bad = 0;
-    for (int s = threadIdx.x; s < p.c.n_slots; s += kPlanThreads) p.claim[s] = 0;
-    __syncthreads();
-    for (int q = threadIdx.x; q < p.n_req; q += kPlanThreads) {
-        const int s = p.slots[q];
-        if (s < 0 || s >= p.c.n_slots) {
-            bad = 1;
-            continue;
-        }
-        if (atomicExch(&p.claim[s], q + 1) != 0) bad = 1;
-        const int n = p.c.lens[s];
-        if (n < 0 || n > p.c.max_pages * p.c.page_size) bad = 1;
-    }
-    __syncthreads();
-    return bad;
+// Names the slot of request q in claim, which is all zero between calls; false when the
+// slot is out of range, named before, or of a length that the cache cannot hold.
+__device__ __forceinline__ bool claim_slot(const PlanParams& p, int s, int* len) {
+    *len = 0;
+    if (s < 0 || s >= p.c.n_slots) return false;
+    const int n = p.c.lens[s];
+    const int before = atomicExch(&p.claim[s], 1);
+    if (before != 0 || n < 0 || n > p.c.max_pages * p.c.page_size) return false;
+    *len = n;
+    return true;
+}
+
+__device__ __forceinline__ void unclaim_slot(const PlanParams& p, int s) {
+    if (s >= 0 && s < p.c.n_slots) p.claim[s] = 0;
+}
+
+constexpr int kCluster = 8;
+
+// Whether any CTA of the cluster has seen something bad.
+__device__ bool cluster_any(int bad) {
+    __shared__ int s_bad[kCluster];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cl = cg::this_cluster();
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x < kCluster) *cl.map_shared_rank(&s_bad[cl.block_rank()], threadIdx.x) = bad;
+    cl.sync();
+    int any = 0;
+    for (int i = 0; i < kCluster; i++) any |= s_bad[i];
+    return any != 0;
 }
 
 __device__ void refuse(const PlanParams& p, int bit) {
@@ -147,24 +163,21 @@ template <bool COMPACT>
 __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(PlanParams p) {
     __shared__ int s_warp[32];
     __shared__ int s_total;
+    allow_next_launch();
     const int tid = threadIdx.x, ps = p.c.page_size;
-    int bad = claim_slots(p);
+    int bad = 0;
     if (tid == 0 && (p.off[0] != 0 || p.off[p.n_req] != p.T)) bad = 1;
-    for (int q = tid; q < p.n_req; q += kPlanThreads) {
-        const int cnt = p.off[q + 1] - p.off[q];
-        if (cnt < 0 || cnt > p.T) bad = 1;
-    }
-    if (__syncthreads_or(bad)) return refuse(p, kStatusBounds);
     // pages each request needs, and its place in the list of free pages
     int carry = 0;
     for (int q0 = 0; q0 < p.n_req; q0 += kPlanThreads) {
         const int q = q0 + tid;
         int need = 0;
         if (q < p.n_req) {
-            const int s = p.slots[q], n = p.c.lens[s], cnt = p.off[q + 1] - p.off[q];
+            const int s = p.slots[q], cnt = p.off[q + 1] - p.off[q];
+            int n, cow = -1;
+            const bool ok = claim_slot(p, s, &n);
             const long long n_new = COMPACT ? cnt : (long long)n + cnt;
-            int cow = -1;
-            if (n_new > (long long)p.c.max_pages * ps) {
+            if (!ok || cnt < 0 || cnt > p.T || n_new > (long long)p.c.max_pages * ps) {
                 bad = 1;
             } else if (COMPACT) {
                 need = pages_of(cnt, ps);
@@ -187,86 +200,157 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(PlanParams p) {
         carry += s_total;
         __syncthreads();
     }
-    if (__syncthreads_or(bad)) return refuse(p, kStatusBounds);
+    bad = __syncthreads_or(bad);
+    for (int q = tid; q < p.n_req; q += kPlanThreads) unclaim_slot(p, p.slots[q]);
+    if (bad) return refuse(p, kStatusBounds);
     if (!find_free(p, carry, s_warp, &s_total)) return refuse(p, kStatusFull);
-    // nothing was changed so far; a warp a request from here
+    // nothing was changed so far; a warp takes four requests at a time from here, so that their
+    // lookups are in flight together
     const int warp = tid >> 5, lane = tid & 31;
-    for (int q = warp; q < p.n_req; q += kPlanThreads / 32) {
-        const int s = p.slots[q], n = p.old_len[q], cnt = p.off[q + 1] - p.off[q];
-        const int* fresh = p.free_list + p.base[q];
-        int32_t* row = p.c.page_table + (size_t)s * p.c.max_pages;
+    for (int q0 = 4 * warp; q0 < p.n_req; q0 += 4 * (kPlanThreads / 32)) {
+        int s[4], n[4], cnt[4], base[4], cow[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int q = min(q0 + i, p.n_req - 1);
+            s[i] = p.slots[q];
+            n[i] = p.old_len[q];
+            cnt[i] = q0 + i < p.n_req ? p.off[q + 1] - p.off[q] : 0;
+            base[i] = p.base[q];
+            cow[i] = p.cow[q];
+        }
         if (COMPACT) {
-            const int n_old = pages_of(n, ps), n_new = pages_of(cnt, ps);
-            int* old = p.old_table + (size_t)q * p.c.max_pages;
-            for (int e = lane; e < max(n_old, n_new); e += 32) {
-                if (e < n_old) {
-                    const int pg = row[e];
-                    old[e] = pg;
-                    if (pg >= 0 && pg < p.c.n_pages) atomicSub(&p.c.ref[pg], 1);
+            const int np = p.c.max_pages;
+            for (int e = lane; e < np; e += 32) {
+                int old[4], fresh[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    old[i] = e < pages_of(n[i], ps) ? p.c.page_table[(size_t)s[i] * np + e] : -1;
+                    fresh[i] = e < pages_of(cnt[i], ps) ? p.free_list[base[i] + e] : -1;
                 }
-                if (e < n_new) p.c.ref[fresh[e]] = 1;
-                row[e] = e < n_new ? fresh[e] : -1;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (q0 + i >= p.n_req || (e >= pages_of(n[i], ps) && fresh[i] < 0)) continue;
+                    p.old_table[(size_t)(q0 + i) * np + e] = old[i];
+                    if (old[i] >= 0 && old[i] < p.c.n_pages) atomicSub(&p.c.ref[old[i]], 1);
+                    if (fresh[i] >= 0) p.c.ref[fresh[i]] = 1;
+                    p.c.page_table[(size_t)s[i] * np + e] = fresh[i];
+                }
             }
-            if (lane == 0) p.c.lens[s] = cnt;
         } else {
-            const int cow = p.cow[q];
-            const int first = pages_of(n, ps) - (cow >= 0 ? 1 : 0), last = pages_of(n + cnt, ps);
-            for (int e = first + lane; e < last; e += 32) {
-                row[e] = fresh[e - first];
-                p.c.ref[fresh[e - first]] = 1;
-            }
-            if (lane == 0) {
-                if (cow >= 0) atomicSub(&p.c.ref[cow], 1);
-                p.c.lens[s] = n + cnt;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int first = pages_of(n[i], ps) - (cow[i] >= 0 ? 1 : 0), last = pages_of(n[i] + cnt[i], ps);
+                if (q0 + i >= p.n_req) continue;
+                for (int e = first + lane; e < last; e += 32) {
+                    const int pg = p.free_list[base[i] + e - first];
+                    p.c.page_table[(size_t)s[i] * p.c.max_pages + e] = pg;
+                    p.c.ref[pg] = 1;
+                }
+                if (lane == 0 && cow[i] >= 0) atomicSub(&p.c.ref[cow[i]], 1);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (lane == i && q0 + i < p.n_req) p.c.lens[s[i]] = COMPACT ? cnt[i] : n[i] + cnt[i];
     }
     if (tid == 0) p.ctrl->valid = 1;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) fork_kernel(PlanParams p) {
-    int bad = claim_slots(p);
-    for (int q = threadIdx.x; q < p.n_req; q += kPlanThreads) {
-        const int a = p.src_slots[q], b = p.slots[q];
-        if (a < 0 || a >= p.c.n_slots) {
-            bad = 1;
-            continue;
+// Threads of the cluster, and this one's number among them.
+constexpr int kClusterThreads = kCluster * kPlanThreads;
+__device__ __forceinline__ int cluster_thread() { return blockIdx.x * kPlanThreads + threadIdx.x; }
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) fork_kernel(PlanParams p) {
+    int bad = 0, n;
+    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads)
+        if (!claim_slot(p, p.slots[q], &n) || n != 0) bad = 1;
+    bool any = cluster_any(bad);                      // all slots are named
+    bad = 0;
+    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) {
+        const int a = p.src_slots[q];
+        if (a < 0 || a >= p.c.n_slots || p.claim[a] != 0) {
+            bad = 1;                                  // a source is no destination
+        } else {
+            n = p.c.lens[a];
+            if (n < 0 || n > p.c.max_pages * p.c.page_size) bad = 1;
         }
-        const int n = p.c.lens[a];
-        if (p.claim[a] != 0 || n < 0 || n > p.c.max_pages * p.c.page_size) bad = 1;   // a source is no destination
-        if (b >= 0 && b < p.c.n_slots && p.c.lens[b] != 0) bad = 1;
     }
-    if (__syncthreads_or(bad)) return refuse(p, kStatusBounds);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int q = warp; q < p.n_req; q += kPlanThreads / 32) {
-        const int a = p.src_slots[q], b = p.slots[q];
-        const int n = p.c.lens[a], np = pages_of(n, p.c.page_size);
-        const int32_t* from = p.c.page_table + (size_t)a * p.c.max_pages;
-        int32_t* to = p.c.page_table + (size_t)b * p.c.max_pages;
-        for (int e = lane; e < np; e += 32) {
-            const int pg = from[e];
-            if (pg >= 0 && pg < p.c.n_pages) atomicAdd(&p.c.ref[pg], 1);
-            to[e] = pg;
+    cooperative_groups::this_cluster().sync();        // the flags of the round before are read
+    any = cluster_any(bad) || any;
+    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) unclaim_slot(p, p.slots[q]);
+    cooperative_groups::this_cluster().sync();        // no CTA leaves while another may write to it
+    if (any) {
+        if (blockIdx.x == 0) refuse(p, kStatusBounds);
+        return;
+    }
+    // a warp takes four requests at a time, so that their lookups are in flight together
+    const int warp = cluster_thread() >> 5, lane = threadIdx.x & 31, np = p.c.max_pages;
+    for (int q0 = 4 * warp; q0 < p.n_req; q0 += 4 * (kClusterThreads / 32)) {
+        int a[4], b[4], n[4], most = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int q = min(q0 + i, p.n_req - 1);
+            a[i] = p.src_slots[q];
+            b[i] = p.slots[q];
         }
-        if (lane == 0) p.c.lens[b] = n;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            n[i] = q0 + i < p.n_req ? p.c.lens[a[i]] : 0;
+            most = max(most, pages_of(n[i], p.c.page_size));
+        }
+        for (int e = lane; e < most; e += 32) {
+            int pg[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) pg[i] = e < pages_of(n[i], p.c.page_size) ? p.c.page_table[(size_t)a[i] * np + e] : -1;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (e < pages_of(n[i], p.c.page_size)) {
+                    if (pg[i] >= 0 && pg[i] < p.c.n_pages) atomicAdd(&p.c.ref[pg[i]], 1);
+                    p.c.page_table[(size_t)b[i] * np + e] = pg[i];
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (lane == i && q0 + i < p.n_req) p.c.lens[b[i]] = n[i];
     }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) free_kernel(PlanParams p) {
-    const int bad = claim_slots(p);
-    if (__syncthreads_or(bad)) return refuse(p, kStatusBounds);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int q = warp; q < p.n_req; q += kPlanThreads / 32) {
-        const int s = p.slots[q];
-        const int np = pages_of(p.c.lens[s], p.c.page_size);
-        int32_t* row = p.c.page_table + (size_t)s * p.c.max_pages;
-        for (int e = lane; e < np; e += 32) {
-            const int pg = row[e];
-            if (pg >= 0 && pg < p.c.n_pages) atomicSub(&p.c.ref[pg], 1);
-            row[e] = -1;
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) free_kernel(PlanParams p) {
+    int bad = 0, n;
+    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads)
+        if (!claim_slot(p, p.slots[q], &n)) bad = 1;
+    const bool any = cluster_any(bad);
+    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) unclaim_slot(p, p.slots[q]);
+    cooperative_groups::this_cluster().sync();        // no CTA leaves while another may write to it
+    if (any) {
+        if (blockIdx.x == 0) refuse(p, kStatusBounds);
+        return;
+    }
+    const int warp = cluster_thread() >> 5, lane = threadIdx.x & 31, np = p.c.max_pages;
+    for (int q0 = 4 * warp; q0 < p.n_req; q0 += 4 * (kClusterThreads / 32)) {
+        int s[4], n[4], most = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) s[i] = p.slots[min(q0 + i, p.n_req - 1)];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            n[i] = q0 + i < p.n_req ? pages_of(p.c.lens[s[i]], p.c.page_size) : 0;
+            most = max(most, n[i]);
+        }
+        for (int e = lane; e < most; e += 32) {
+            int pg[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) pg[i] = e < n[i] ? p.c.page_table[(size_t)s[i] * np + e] : -1;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (e < n[i]) {
+                    if (pg[i] >= 0 && pg[i] < p.c.n_pages) atomicSub(&p.c.ref[pg[i]], 1);
+                    p.c.page_table[(size_t)s[i] * np + e] = -1;
+                }
         }
         __syncwarp();
-        if (lane == 0) p.c.lens[s] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (lane == i && q0 + i < p.n_req) p.c.lens[s[i]] = 0;
     }
 }
 
@@ -302,6 +386,7 @@ __device__ __forceinline__ int request_of(const int32_t* off, int n_req, int r) 
 // of the shared pages that are copied before they are written on.
 template <bool COMPACT>
 __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(CopyParams p) {
+    wait_for_prior_launch();
     if (p.ctrl->valid == 0) return;
     const int lane = threadIdx.x & 31, ps = p.c.page_size;
     const long long warp0 = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) >> 5;
@@ -387,9 +472,8 @@ int launch_copy(bool compact, const CopyParams& p, cudaStream_t s) {
     const long long warps = (rows + kRowsPerWarp - 1) / kRowsPerWarp;
     const long long blocks = std::min<long long>((warps * 32 + kCopyThreads - 1) / kCopyThreads, 148LL * 2);   // one resident wave
     if (blocks < 1) return HSTU_OK;
-    if (compact) copy_rows_kernel<true><<<(int)blocks, kCopyThreads, 0, s>>>(p);
-    else copy_rows_kernel<false><<<(int)blocks, kCopyThreads, 0, s>>>(p);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(compact ? launch_early(copy_rows_kernel<true>, (int)blocks, kCopyThreads, 0, s, p)
+                               : launch_early(copy_rows_kernel<false>, (int)blocks, kCopyThreads, 0, s, p));
 }
 
 // Checks common to the operators; *p gets the plan's parameters.
@@ -500,7 +584,7 @@ int hstu_cache_fork(const hstu_page_cache* cache, int32_t n_req, const int32_t* 
     if (n_req == 0) return HSTU_OK;
     if (!aligned(src_slots, 4)) return HSTU_ERR_INVALID_ARG;
     p.src_slots = src_slots;
-    fork_kernel<<<1, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    fork_kernel<<<kCluster, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -510,6 +594,6 @@ int hstu_cache_free(const hstu_page_cache* cache, int32_t n_req, const int32_t* 
     const int st = plan_params(cache, n_req, slots, workspace, workspace_bytes, &p);
     if (st != HSTU_OK) return st;
     if (n_req == 0) return HSTU_OK;
-    free_kernel<<<1, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    free_kernel<<<kCluster, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return cuda_status(cudaGetLastError());
 }

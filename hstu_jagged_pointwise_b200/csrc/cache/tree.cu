@@ -57,11 +57,6 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kPrepThreads = 256;
 constexpr int kNarrow = 64, kWide = 128;   // nodes of a group in the two forms
 
-// The launch before this one has completed, and its writes are visible.
-__device__ __forceinline__ void wait_for_prior_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The next launch may start: it waits by wait_for_prior_launch before it reads our results.
-__device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Control block: n_items and counter of tree_attn's work list, valid = -1 after a bad tree
 // or a timeout, pad[0] CTAs of tree_attn that are done, pad[1] = valid for tree_finish.  The
 // last CTA of tree_attn sets pad[1] and clears the others for the next call.
@@ -1246,22 +1241,6 @@ int prepare_device(int* sms) {
     }
     *sms = known[dev];
     return HSTU_OK;
-}
-
-// Launch that may start while the one before it in the stream ends.
-template <typename... Args>
-cudaError_t launch_early(void (*kernel)(Args...), int grid, int block, uint32_t smem, cudaStream_t s, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int D, bool WIDE>

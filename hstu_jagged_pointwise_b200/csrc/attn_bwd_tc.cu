@@ -902,14 +902,26 @@ __global__ void scale_bf16_kernel(const uint4* __restrict__ src, uint4* __restri
     }
 }
 
-// d_rab[i] = sum over CTAs of part[cta][i], in CTA order.
-__global__ void rab_reduce_kernel(const float* __restrict__ part, int n_part, int P, int nb,
-                                  float* __restrict__ d_rab_pos, float* __restrict__ d_rab_time) {
+// d_rab[i] = sum over CTAs of part[cta][i], in CTA order: 32 entries a block, their parts
+// brought to shared memory by all its warps first, so that the ordered sum of 148 of them
+// costs additions and not a chain of loads (6.7 us a launch without, 4.3 with).
+constexpr int kRabCols = 32, kRabRows = 256;
+__global__ void __launch_bounds__(256) rab_reduce_kernel(const float* __restrict__ part, int n_part, int P, int nb,
+                                                         float* __restrict__ d_rab_pos, float* __restrict__ d_rab_time) {
+    __shared__ float s_part[kRabRows][kRabCols];
     const int w = 2 * P - 1 + nb;
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= w) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * kRabCols + lane;
     float s = 0.f;
-    for (int c = 0; c < n_part; c++) s += part[(size_t)c * w + i];
+    for (int c0 = 0; c0 < n_part; c0 += kRabRows) {
+        const int n = min(kRabRows, n_part - c0);
+        __syncthreads();
+#pragma unroll 8
+        for (int c = warp; c < n; c += 8) s_part[c][lane] = i < w ? part[(size_t)(c0 + c) * w + i] : 0.f;
+        __syncthreads();
+        if (warp == 0)
+            for (int c = 0; c < n; c++) s += s_part[c][lane];
+    }
+    if (warp != 0 || i >= w) return;
     if (i < 2 * P - 1) d_rab_pos[i] = s;
     else d_rab_time[i - (2 * P - 1)] = s;
 }
@@ -920,7 +932,7 @@ cudaError_t launch_rab_reduce(const float* part, int n_part, int P, int nb, floa
                               float* d_rab_time, cudaStream_t s) {
     const int w = 2 * P - 1 + nb;
     prof_begin(kProfRabReduce, s);
-    rab_reduce_kernel<<<(w + 127) / 128, 128, 0, s>>>(part, n_part, P, nb, d_rab_pos, d_rab_time);
+    rab_reduce_kernel<<<(w + kRabCols - 1) / kRabCols, 256, 0, s>>>(part, n_part, P, nb, d_rab_pos, d_rab_time);
     prof_end(kProfRabReduce, s);
     return cudaGetLastError();
 }

@@ -145,6 +145,150 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(SimtParams p) {
     }
 }
 
+// ------------------------------------------------------------------ forward, window kind
+// The same sums with register tiles, for rows that see a window and the sinks: 32 rows a
+// block, so that short rows fill more SMs, and only the key tiles between.  Thread (rg, kg)
+// of 16 x 16 takes rows 2rg, 2rg+1 against keys kg + 16i (i < 4) for the scores, and columns
+// kg*(D/16).. for the sum with V; 16-byte loads from shared memory feed 8 products each (the
+// kernel above issues two 4-byte loads a product).  4 rows of up to 255 tokens, W = 32, d =
+// 32: 13.9 us against its 45.8.
+constexpr int kWM = 32;
+
+template <int D>
+struct WinSmem {
+    static constexpr int LD = D + 4;
+    static constexpr int LP = kBN + 4;
+    static constexpr size_t bytes = (size_t)(kWM * LD + 2 * kBN * LD + kWM * LP + 2 * kMaxPos + kMaxTBuckets) * 4 + kBN * 8;
+};
+
+template <int D>
+__device__ __forceinline__ void load_rows4(float* dst, const float* src, int ld, const SeqCtx& c, int r0, int rows, int h) {
+    constexpr int V = D / 4;
+    for (int e = threadIdx.x; e < rows * V; e += kThreads) {
+        const int r = e / V, col = 4 * (e % V), i = r0 + r;
+        const float4 x = i < c.L ? *reinterpret_cast<const float4*>(src + (size_t)(c.off0 + i) * ld + (size_t)h * D + col)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(dst + r * WinSmem<D>::LD + col) = x;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) attn_fwd_simt_window_kernel(SimtParams p) {
+    using Sm = WinSmem<D>;
+    constexpr int LD = Sm::LD, LP = Sm::LP, NC = D / 16;
+    extern __shared__ float smf[];
+    int64_t* sTsK = reinterpret_cast<int64_t*>(smf);
+    float* sQ = smf + 2 * kBN;
+    float* sK = sQ + kWM * LD;
+    float* sV = sK + kBN * LD;
+    float* sP = sV + kBN * LD;
+    float* s_rp = sP + kWM * LP;
+    float* s_rt = s_rp + 2 * kMaxPos;
+
+    const int b = blockIdx.z, h = blockIdx.y, row0 = blockIdx.x * kWM;
+    if (!p.ctrl->valid) return;
+    const SeqCtx c = seq_ctx(p, b);
+    if (row0 >= c.L) return;
+    const int ld = p.H * D;
+    load_tables(s_rp, s_rt, p);
+    load_rows4<D>(sQ, static_cast<const float*>(p.q), ld, c, row0, kWM, h);
+    const int rg = threadIdx.x >> 4, kg = threadIdx.x & 15;
+    int64_t ts_i[2];
+#pragma unroll
+    for (int a = 0; a < 2; a++) ts_i[a] = p.ts[c.off0 + min(row0 + 2 * rg + a, c.L - 1)];
+    float acc[2][NC];
+#pragma unroll
+    for (int a = 0; a < 2; a++)
+#pragma unroll
+        for (int e = 0; e < NC; e++) acc[a][e] = 0.f;
+
+    const int qb = min(row0 + kWM - 1, c.L - 1);
+    for (int t = 0; t * kBN <= qb; t++) {
+        const int n0 = t * kBN;
+        if (tile_class(HSTU_KIND_WINDOW, row0, qb, n0, min(n0 + kBN - 1, c.L - 1), c.S, c.R) == 0) {
+            t = max(t, max(row0 - c.R + 1, 0) / kBN - 1);         // past the sinks: on to the window
+            continue;
+        }
+        __syncthreads();
+        load_rows4<D>(sK, static_cast<const float*>(p.k), ld, c, n0, kBN, h);
+        load_rows4<D>(sV, static_cast<const float*>(p.v), ld, c, n0, kBN, h);
+        if (threadIdx.x < kBN) sTsK[threadIdx.x] = n0 + (int)threadIdx.x < c.L ? p.ts[c.off0 + n0 + threadIdx.x] : 0;
+        __syncthreads();
+        float s[2][4] = {};
+#pragma unroll 4
+        for (int e = 0; e < D; e += 4) {
+            float4 q[2], k[4];
+#pragma unroll
+            for (int a = 0; a < 2; a++) q[a] = *reinterpret_cast<const float4*>(sQ + (2 * rg + a) * LD + e);
+#pragma unroll
+            for (int i = 0; i < 4; i++) k[i] = *reinterpret_cast<const float4*>(sK + (kg + 16 * i) * LD + e);
+#pragma unroll
+            for (int a = 0; a < 2; a++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    s[a][i] = fmaf(q[a].x, k[i].x, s[a][i]);
+                    s[a][i] = fmaf(q[a].y, k[i].y, s[a][i]);
+                    s[a][i] = fmaf(q[a].z, k[i].z, s[a][i]);
+                    s[a][i] = fmaf(q[a].w, k[i].w, s[a][i]);
+                }
+        }
+#pragma unroll
+        for (int a = 0; a < 2; a++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = row0 + 2 * rg + a, jl = kg + 16 * i, j = n0 + jl;
+                const bool vis = r < c.L && j < c.L && visible(HSTU_KIND_WINDOW, r, j, c.S, c.R, 0, 0);
+                const float z = s[a][i] + s_rp[pos_index(r, j, p.P)] + s_rt[time_bucket(ts_i[a], sTsK[jl], p.nb)];
+                sP[(2 * rg + a) * LP + jl] = vis ? z * sigmoid_acc(z) : 0.f;
+            }
+        __syncthreads();
+#pragma unroll 4
+        for (int jl = 0; jl < kBN; jl += 4) {
+            float w[2][4];
+#pragma unroll
+            for (int a = 0; a < 2; a++) {
+                const float4 x = *reinterpret_cast<const float4*>(sP + (2 * rg + a) * LP + jl);
+                w[a][0] = x.x; w[a][1] = x.y; w[a][2] = x.z; w[a][3] = x.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float v[NC];
+#pragma unroll
+                for (int e = 0; e < NC; e += 2) {
+                    const float2 x = *reinterpret_cast<const float2*>(sV + (jl + i) * LD + kg * NC + e);
+                    v[e] = x.x;
+                    v[e + 1] = x.y;
+                }
+#pragma unroll
+                for (int a = 0; a < 2; a++)
+#pragma unroll
+                    for (int e = 0; e < NC; e++) acc[a][e] = fmaf(w[a][i], v[e], acc[a][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < 2; a++) {
+        const int r = row0 + 2 * rg + a;
+        if (r < c.L) {
+            float* y = static_cast<float*>(p.y) + (size_t)(c.off0 + r) * ld + (size_t)h * D + kg * NC;
+#pragma unroll
+            for (int e = 0; e < NC; e += 2)
+                *reinterpret_cast<float2*>(y + e) = make_float2(acc[a][e] * p.inv_alpha, acc[a][e + 1] * p.inv_alpha);
+        }
+    }
+}
+
+template <int D>
+cudaError_t fwd_window_one(const SimtParams& p, cudaStream_t s) {
+    cudaError_t e = ensure_smem_limit((const void*)attn_fwd_simt_window_kernel<D>, (int)WinSmem<D>::bytes);
+    if (e != cudaSuccess) return e;
+    dim3 grid((p.max_len + kWM - 1) / kWM, p.H, p.B);
+    prof_begin(kProfAttnFwdSimt, s);
+    attn_fwd_simt_window_kernel<D><<<grid, kThreads, WinSmem<D>::bytes, s>>>(p);
+    prof_end(kProfAttnFwdSimt, s);
+    return cudaGetLastError();
+}
+
 // One (query tile, key tile) block of the backward: fills sA = mask*SiLU(z)/alpha and
 // sDZ = dz for rows [qa, qa+64) x cols [ka, ka+64).  Thread (x, cg) handles pair
 // rows/cols given by the caller's mapping.
@@ -366,6 +510,11 @@ cudaError_t bwd_one(const SimtParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attn_fwd_simt(int dtype_f32, int d, const SimtParams& p, cudaStream_t s) {
+    if (dtype_f32 && p.kind == HSTU_KIND_WINDOW) {
+        if (d == 32) return fwd_window_one<32>(p, s);
+        if (d == 64) return fwd_window_one<64>(p, s);
+        if (d == 128) return fwd_window_one<128>(p, s);
+    }
     if (dtype_f32) {
         if (d == 32) return fwd_one<float, 32>(p, s);
         if (d == 64) return fwd_one<float, 64>(p, s);

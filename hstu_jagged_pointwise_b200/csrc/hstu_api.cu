@@ -464,8 +464,12 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int D = d.H * d.d_v;
-    cudaError_t e = cudaMemsetAsync(d_rab_pos, 0, sizeof(float) * (2 * d.n_pos - 1), s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(d_rab_time, 0, sizeof(float) * d.n_tbuckets, s);
+    // (the tensor-core backward's last step writes both tables whole)
+    cudaError_t e = cudaSuccess;
+    if (d.T == 0 || d.dtype == HSTU_F32) {
+        e = cudaMemsetAsync(d_rab_pos, 0, sizeof(float) * (2 * d.n_pos - 1), s);
+        if (e == cudaSuccess) e = cudaMemsetAsync(d_rab_time, 0, sizeof(float) * d.n_tbuckets, s);
+    }
     if (e == cudaSuccess && d.T == 0 && !from_dy) {
         e = cudaMemsetAsync(d_gamma, 0, sizeof(float) * D * G, s);
         if (e == cudaSuccess) e = cudaMemsetAsync(d_beta, 0, sizeof(float) * D * G, s);

@@ -1068,6 +1068,13 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(TreeParams 
     wait_for_prior_launch();
     if (p.ctrl->pad[kVerdict] != 0) return;
     const int4 nd = p.node[cc];                      // position, parent's row, tree, splits
+    float4 part0[NV][2];                             // the first split's sums, on their way while the path is worked
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+        if (in(i)) {
+            part0[i][0] = __ldcs(reinterpret_cast<const float4*>(p.part + row + col(i)));
+            part0[i][1] = __ldcs(reinterpret_cast<const float4*>(p.part + row + col(i)) + 1);
+        }
     const int S = p.window ? p.n_sink[nd.z] : 0, W = p.window ? p.window[nd.z] : 0x7fffffff;
     // the path: c itself, then its ancestors
     int64_t ts_a = ts_c;
@@ -1107,7 +1114,8 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(TreeParams 
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (in(i)) {
-                const float4 x = __ldcs(reinterpret_cast<const float4*>(part + col(i))), y = __ldcs(reinterpret_cast<const float4*>(part + col(i)) + 1);
+                const float4 x = sp == 0 ? part0[i][0] : __ldcs(reinterpret_cast<const float4*>(part + col(i)));
+                const float4 y = sp == 0 ? part0[i][1] : __ldcs(reinterpret_cast<const float4*>(part + col(i)) + 1);
                 acc[i][0] += x.x; acc[i][1] += x.y; acc[i][2] += x.z; acc[i][3] += x.w;
                 acc[i][4] += y.x; acc[i][5] += y.y; acc[i][6] += y.z; acc[i][7] += y.w;
             }

@@ -99,6 +99,8 @@ constexpr uint32_t kHalfPanel = 64u * 128u;                      // 64 rows x 12
 struct KvItem {
     int b, n0, h, n_end;   // keys [n0, n_end) of sequence b, head h
     int off0, L, S, R;
+    int t0, t1;            // query tiles it may see: [t0, t1)
+    int chunk;             // window kind: chunk of the sinks' key tile, or -1
 };
 
 template <int KIND>
@@ -108,6 +110,15 @@ __device__ __forceinline__ KvItem load_kv_item(const BwdParams& p, int4 it) {
     s.off0 = p.off[s.b];
     s.L = p.off[s.b + 1] - s.off0;
     segment_sizes(KIND, p.n_static, p.n_rt, s.b, s.L, &s.S, &s.R);
+    s.t0 = KIND == HSTU_KIND_WINDOW ? s.n0 / kTileM : 0;
+    s.t1 = (s.L + kTileM - 1) / kTileM;
+    s.chunk = -1;
+    if (KIND == HSTU_KIND_WINDOW && it.z >= 256) {
+        s.h = it.z & 255;
+        s.chunk = (it.z >> 8) - 1;
+        s.t0 = s.chunk * kSinkChunk;
+        s.t1 = min(s.t1, s.t0 + kSinkChunk);
+    }
     return s;
 }
 
@@ -126,7 +137,7 @@ __device__ __forceinline__ int next_visible(const KvItem& s, int t, int n_qt) {
     if (KIND == HSTU_KIND_CAUSAL && t >= 0) return t + 1 < n_qt ? t + 1 : n_qt;
     // window: the tiles that see it are one run that starts at the key tile's own
     if (KIND == HSTU_KIND_WINDOW) {
-        t = t < 0 ? s.n0 / kTileM : t + 1;
+        t = t < 0 ? s.t0 : t + 1;
         return t < n_qt && q_class<KIND>(s, t) != 0 ? t : n_qt;
     }
     for (t++; t < n_qt; t++)
@@ -350,9 +361,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     kv_use++;
                 }
-                const int n_qt = (s.L + kTileM - 1) / kTileM;
+                const int n_qt = s.t1;
                 int t_pf = 0;                              // next query tile to prefetch into L2
-                for (int t = KIND == HSTU_KIND_WINDOW ? s.n0 / kTileM : 0; ok && t < n_qt; t++) {
+                for (int t = s.t0; ok && t < n_qt; t++) {
                     if (q_class<KIND>(s, t) == 0) {
                         if (KIND == HSTU_KIND_WINDOW) break;   // the visible tiles are one run
                         continue;
@@ -501,7 +512,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (it.x < 0) break;
             if (lane == 0) {
                 const KvItem s = load_kv_item<KIND>(p, it);
-                const int n_qt = (s.L + kTileM - 1) / kTileM;
+                const int n_qt = s.t1;
                 ok = mbar_wait(&bars[kKVFull], kv_use & 1, s_abort, p.dbg.limit);
                 kv_use++;
                 int t = next_visible<KIND>(s, -1, n_qt);
@@ -580,7 +591,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int32_t a_j = (int32_t)(uint32_t)((uint64_t)ts_j - (uint64_t)kmin);
             // |kmin| < 2^62: then tq - kmin cannot wrap to a small value unless it is small
             const bool kmin_ok = (uint64_t)kmin + (1ull << 62) < (1ull << 63);
-            const int n_qt = (s.L + kTileM - 1) / kTileM;
+            const int n_qt = s.t1;
             int n_done = 0;
             int t = next_visible<KIND>(s, -1, n_qt), t_prev = -1;
             // ---- drain dQ^T_hh of query tile tq (lanes = head dims, columns = queries): one slab
@@ -828,7 +839,19 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tmem_ld16(tmem + lane_base + kKCol + col, kv);
                 tmem_ld_wait(vv);
                 tmem_ld_wait(kv);
-                if (key_ok) {
+                if (KIND == HSTU_KIND_WINDOW && s.chunk >= 0) {
+                    // a chunk of the sinks' key tile: its share of the sums, all 128 rows
+                    float* part = p.sink_part + (((size_t)(sink_place(s.off0) + s.chunk) * p.H + s.h) * 2 * 128 + r) * D + col;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float vs = p.inv_alpha;
+                        *reinterpret_cast<float4*>(part + e) = make_float4(__uint_as_float(kv[e]), __uint_as_float(kv[e + 1]),
+                                                                           __uint_as_float(kv[e + 2]), __uint_as_float(kv[e + 3]));
+                        *reinterpret_cast<float4*>(part + 128 * D + e) =
+                            make_float4(vs * __uint_as_float(vv[e]), vs * __uint_as_float(vv[e + 1]), vs * __uint_as_float(vv[e + 2]),
+                                        vs * __uint_as_float(vv[e + 3]));
+                    }
+                } else if (key_ok) {
                     uint4 wv[2], wk[2];
                     uint32_t* pv = reinterpret_cast<uint32_t*>(wv);
                     uint32_t* pk = reinterpret_cast<uint32_t*>(wk);
@@ -902,6 +925,27 @@ __global__ void scale_bf16_kernel(const uint4* __restrict__ src, uint4* __restri
     }
 }
 
+// Four rows of a (sequence, head)'s first key tile a block (256 threads at d = 128), four columns of
+// dK or dV a thread, summed over the chunks in order.
+template <int D>
+__global__ void __launch_bounds__(2 * D) sink_reduce_kernel(BwdParams p) {
+    if (!p.ctrl->valid) return;
+    const int b = blockIdx.y, h = blockIdx.x >> 5;
+    const int off = p.off[b], L = p.off[b + 1] - off, n = sink_chunks(L, p.n_static[b]);
+    if (n == 1) return;                                   // the item wrote its rows itself
+    const int e = threadIdx.x, which = e / D, row = 4 * (blockIdx.x & 31) + e / (D / 4) % 4, c = 4 * (e % (D / 4));
+    const float* src = p.sink_part + ((((size_t)sink_place(off) * p.H + h) * 2 + which) * 128 + row) * D + c;
+    const size_t step = (size_t)p.H * 2 * 128 * D;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < n; k++) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(src + k * step));
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    __nv_bfloat16* out = (which ? p.dv : p.dk) + (size_t)(off + row) * p.ld + (size_t)h * D + c;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+}
+
 // d_rab[i] = sum over CTAs of part[cta][i], in CTA order: 32 entries a block, their parts
 // brought to shared memory by all its warps first, so that the ordered sum of 148 of them
 // costs additions and not a chain of loads (6.7 us a launch without, 4.3 with).
@@ -927,6 +971,20 @@ __global__ void __launch_bounds__(256) rab_reduce_kernel(const float* __restrict
 }
 
 }  // namespace
+
+cudaError_t launch_sink_reduce(int d, int B, const BwdParams& p, cudaStream_t s) {
+    prof_begin(kProfSinkReduce, s);
+    for (int b0 = 0; b0 < B; b0 += 65535) {               // a grid's y extent
+        BwdParams q = p;
+        q.off = p.off + b0;
+        q.n_static = p.n_static + b0;
+        const dim3 grid(32 * p.H, B - b0 < 65535 ? B - b0 : 65535);
+        if (d == 128) sink_reduce_kernel<128><<<grid, 256, 0, s>>>(q);
+        else sink_reduce_kernel<64><<<grid, 128, 0, s>>>(q);
+    }
+    prof_end(kProfSinkReduce, s);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_rab_reduce(const float* part, int n_part, int P, int nb, float* d_rab_pos,
                               float* d_rab_time, cudaStream_t s) {

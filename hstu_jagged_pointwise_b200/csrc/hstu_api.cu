@@ -147,15 +147,19 @@ int check_mask(const hstu_mask_spec* m, int* kind) {
 
 // ------------------------------------------------------------------ workspace layout
 struct Layout {
-    size_t items = 0, perm = 0, seq_base = 0, dy = 0, part = 0, dq_acc = 0, rab_part = 0, gmask = 0, total = 0;
+    size_t items = 0, perm = 0, seq_base = 0, dy = 0, part = 0, dq_acc = 0, rab_part = 0, sink_part = 0, gmask = 0, total = 0;
     long long max_items = 0;
     int n_part = 0;
 };
 
-Layout attn_layout(const hstu_dims& d, int is_bwd, int n_groups = 1) {
+Layout attn_layout(const hstu_dims& d, int is_bwd, bool window, int n_groups = 1) {
     Layout L;
     size_t off = sizeof(Control);
     L.max_items = (long long)d.H * (((long long)d.T + kTileM - 1) / kTileM + d.B);
+    // the window backward cuts the sinks' key tile of sequences longer than a chunk
+    const bool cut = window && is_bwd && d.dtype == HSTU_BF16;
+    const long long sink_places = cut ? 2 * ((long long)d.T / (kTileM * kSinkChunk) + 1) : 0;
+    L.max_items += d.H * sink_places;
     L.items = off;
     off = align_up(off + (size_t)L.max_items * sizeof(int4), 256);
     L.perm = off;
@@ -179,6 +183,8 @@ Layout attn_layout(const hstu_dims& d, int is_bwd, int n_groups = 1) {
             off = align_up(off + (size_t)d.T * D * 4, 256);
             L.rab_part = off;                    // per-CTA rab gradient partial sums
             off = align_up(off + (size_t)kMaxBwdCtas * (2 * d.n_pos - 1 + d.n_tbuckets) * 4, 256);
+            L.sink_part = off;
+            off = align_up(off + (size_t)sink_places * D * 2 * kTileN * 4, 256);
         }
     }
     L.total = off;
@@ -293,14 +299,14 @@ size_t hstu_attn_workspace_bytes(const hstu_dims* dims, int32_t mask_kind, int32
         mask_kind != HSTU_MASK_WINDOW)
         return 0;
     if (is_bwd && mask_kind == HSTU_MASK_MFALCON_SEQ) return 0;
-    return attn_layout(*dims, is_bwd ? 1 : 0).total;
+    return attn_layout(*dims, is_bwd ? 1 : 0, mask_kind == HSTU_MASK_WINDOW).total;
 }
 
 size_t hstu_attn_workspace_bytes_gln(const hstu_dims* dims, int32_t mask_kind, int32_t n_groups, int32_t is_bwd) {
     if (n_groups < 1 || n_groups > kLnMaxGroups) return 0;
     if (hstu_attn_workspace_bytes(dims, mask_kind, is_bwd) == 0) return 0;
     if ((long long)n_groups * dims->H * dims->d_v > kLnMaxGroupCols) return 0;
-    return attn_layout(*dims, is_bwd ? 1 : 0, n_groups).total;
+    return attn_layout(*dims, is_bwd ? 1 : 0, mask_kind == HSTU_MASK_WINDOW, n_groups).total;
 }
 
 namespace {
@@ -336,7 +342,7 @@ int attn_fwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
     st = check_mask(mask, &kind);
     if (st != HSTU_OK) return st;
     const hstu_dims& d = *dims;
-    const Layout L = attn_layout(d, 0, G);
+    const Layout L = attn_layout(d, 0, kind == HSTU_KIND_WINDOW, G);
     if (!aligned(workspace, 256)) return HSTU_ERR_WORKSPACE;
     if (workspace_bytes < L.total) return HSTU_ERR_WORKSPACE;
     if (d.T == 0) return HSTU_OK;
@@ -444,7 +450,7 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
     if (st != HSTU_OK) return st;
     if (kind == HSTU_KIND_MFSEQ) return HSTU_ERR_UNSUPPORTED;   // scoring pass: forward only
     const hstu_dims& d = *dims;
-    const Layout L = attn_layout(d, 1, G);
+    const Layout L = attn_layout(d, 1, kind == HSTU_KIND_WINDOW, G);
     if (!aligned(workspace, 256)) return HSTU_ERR_WORKSPACE;
     if (workspace_bytes < L.total) return HSTU_ERR_WORKSPACE;
     if (!aligned(d_rab_pos, 4) || !aligned(d_rab_time, 4) ||
@@ -490,6 +496,7 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
     sp.n_rt = mask->n_realtime;
     sp.max_q_len = sp.max_kv_len = d.max_seq_len;
     sp.b_m = 1;
+    sp.cut = kind == HSTU_KIND_WINDOW && d.dtype == HSTU_BF16;
     sp.ascending = 1;        // backward items are key tiles: the first one is seen by most queries
     sp.ctrl = ctrl;
     sp.items = at<int4>(workspace, L.items);
@@ -592,8 +599,13 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
     bp.nb = d.n_tbuckets;
     bp.ld = D;
     bp.inv_alpha = 1.0f / d.alpha;
+    bp.sink_part = at<float>(workspace, L.sink_part);
     st = cuda_status(launch_attn_bwd_tc(kind, d.d_qk, tq, tk, tv, tdy, tdq, bp, grid, s));
     if (st != HSTU_OK) return st;
+    if (kind == HSTU_KIND_WINDOW && d.max_seq_len > kTileM * kSinkChunk) {
+        st = cuda_status(launch_sink_reduce(d.d_qk, d.B, bp, s));
+        if (st != HSTU_OK) return st;
+    }
     st = cuda_status(launch_rab_reduce(rab_part, grid, d.n_pos, d.n_tbuckets, d_rab_pos, d_rab_time, s));
     if (st != HSTU_OK) return st;
     return cuda_status(launch_f32_to_bf16(dq_acc, static_cast<__nv_bfloat16*>(dq), (long long)d.T * D, s));

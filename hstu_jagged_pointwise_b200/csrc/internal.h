@@ -55,6 +55,7 @@ struct SchedParams {
     const int32_t* n_static;
     const int32_t* n_rt;
     int max_q_len, max_kv_len, b_m;
+    int cut;         // window kind, bf16 backward: the sinks' key tile in chunks of kSinkChunk query tiles
     int ascending;   // causal/MTGR tile order inside a group: 1 = first tile first (backward key tiles)
     Control* ctrl;
     int4* items;
@@ -99,6 +100,7 @@ struct BwdParams {
     float* rab_part;          // [grid][2P-1 + nb] per-CTA rab gradient partial sums, zeroed
     int H, P, nb, ld;
     float inv_alpha;          // 1 / alpha (window kind, which reads dY unscaled)
+    float* sink_part;         // window kind: [place][H][dK, dV][128][d] of the sinks' key tile, by chunk
     DebugWait dbg;
 };
 
@@ -203,7 +205,7 @@ enum ProfKind {
     kProfSchedule = 0, kProfAttnFwdTc, kProfAttnFwdSimt, kProfLnFwd, kProfLnBwd, kProfLnBwdReduce,
     kProfAttnBwdDkvSimt, kProfAttnBwdDqSimt, kProfDebugIndices, kProfAttnBwdTc, kProfDqConvert,
     kProfRabReduce, kProfCacheScan, kProfCacheCopy, kProfGemm, kProfSiluGrad, kProfColSum, kProfSlSample, kProfGather,
-    kProfScaleDy, kProfKinds
+    kProfScaleDy, kProfSinkReduce, kProfKinds
 };
 void prof_begin(int kind, cudaStream_t s);
 void prof_end(int kind, cudaStream_t s);
@@ -225,6 +227,8 @@ constexpr int kBwdEwCols = 16;
 cudaError_t launch_attn_bwd_tc(int kind, int d, const CUtensorMap& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, const CUtensorMap& tdy, const CUtensorMap& tdq,
                                const BwdParams& p, int grid, cudaStream_t s);
+// dK and dV of the first key tile of every cut sequence: the sums over its chunks, in order.
+cudaError_t launch_sink_reduce(int d, int B, const BwdParams& p, cudaStream_t s);
 cudaError_t launch_f32_to_bf16(const float* src, __nv_bfloat16* dst, long long n, cudaStream_t s);
 // dst = bf16(src * scale), n a multiple of 8 (16-byte vectors)
 cudaError_t launch_scale_bf16(const __nv_bfloat16* src, __nv_bfloat16* dst, float scale, long long n,

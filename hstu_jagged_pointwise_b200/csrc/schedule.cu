@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
         int nt = 0;
         if (r < p.B) {
             const int b = p.perm[r];
-            nt = n_q_tiles(p, p.q_off[b + 1] - p.q_off[b]);
+            const int L = p.q_off[b + 1] - p.q_off[b];
+            nt = n_q_tiles(p, L) + (p.cut ? sink_chunks(L, p.n_static[b]) - 1 : 0);
         }
         const int ex = block_exclusive_scan(nt, warp_sums, &s_total);
         if (r < p.B) p.seq_base[r] = s_carry + ex;
@@ -168,11 +169,18 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
     for (int r = warp; r < p.B; r += kThreads / 32) {
         const int b = p.perm[r];
         const int Lq = p.q_off[b + 1] - p.q_off[b];
-        const int nt = n_q_tiles(p, Lq);
+        const int nc = p.cut ? sink_chunks(Lq, p.n_static[b]) : 1;
+        const int nt = n_q_tiles(p, Lq) + nc - 1;
         const long long base = (long long)p.seq_base[r] * p.H;
         for (int e = lane; e < nt * p.H; e += 32) {
             const int h = e / nt, k = e % nt;
             int row0, row_end;
+            if (nc > 1) {
+                // chunk k of the first key tile, then the other key tiles
+                const int t = max(k - nc + 1, 0);
+                p.items[base + e] = make_int4(b, t * kTileM, k < nc ? h | (k + 1) << 8 : h, min((t + 1) * kTileM, Lq));
+                continue;
+            }
             tile_rows(p, Lq, nt, k, &row0, &row_end);
             p.items[base + e] = make_int4(b, row0, h, row_end);
         }

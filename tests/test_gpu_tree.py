@@ -379,3 +379,44 @@ def test_python_checks():
         s.score(q, k, v, u, rp, rt, g, b, out=dict(y=q.float(), o_pre=q))
     with pytest.raises(Exception):
         ops.TreeScorer(c.cache, s.slots, s.node_offsets, s.parent, s.node_ts, 2, 64, 1.0, 3)      # H*d is not the cache's
+
+
+def test_pool_past_32_bit_offsets():
+    """A pool of 5 GB for keys and as much for values, whose low pages are taken: pages at its end are
+    filled, forked, cut and scored."""
+    from hstu_jagged_pointwise_b200 import ops
+    n_pages, ps, H, d = 20500, 128, 8, 128
+    D = H * d
+    cache = ops.PagedCache(n_pages, ps, 3, 8, D)
+    assert cache.k.numel() * 2 > 2**32
+    cache.ref[:20480] = 1
+    c = Case([300], [3], H, d, 64, seed=21)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    hk, hv, ts = c.hk[0].cuda(), c.hv[0].cuda(), torch.as_tensor(c.hts[0]).cuda()
+    cache.append(i32(0), i32(0, 300), hk, hv, ts)
+    cache.fork(i32(0), i32(1))
+    cache.compact(i32(1), i32(0, 300), torch.arange(300, dtype=torch.int32, device="cuda"))
+    assert cache.check_device_error() == 0
+    assert cache.page_table[0, :3].tolist() == [20480, 20481, 20482] and cache.page_table[1, :3].tolist() == [20483, 20484, 20485]
+    assert torch.equal(cache.k[20483:20486].reshape(-1, D)[:300], hk) and torch.equal(cache.v[20480:20483].reshape(-1, D)[:300], hv)
+    for slot in (0, 1):
+        s = ops.TreeScorer(cache, i32(slot), torch.as_tensor(c.off).cuda(), torch.as_tensor(c.parent).cuda(), torch.as_tensor(c.node_ts).cuda(),
+                           H, d, c.alpha, 3)
+        out = s.score(*c.tensors())
+        assert s.check_device_error() == 0
+        c.check(out)
+
+
+def test_rows_and_tables_of_other_callers_are_left_alone():
+    """Slots that a call does not name, pages of others and rows behind the last keep their bits."""
+    c = Case([70, 33, 100], [4, 2, 3], 1, 64, 32, seed=14)
+    before = [t.clone() for t in (c.cache.k, c.cache.v, c.cache.ts, c.cache.page_table, c.cache.lens, c.cache.ref)]
+    out = dict(y=torch.full((c.T + 5, c.D), 9.0, dtype=torch.bfloat16, device="cuda"), o_pre=torch.full((c.T + 5, c.D), 9.0, dtype=torch.bfloat16, device="cuda"))
+    s = c.scorer()
+    s.score(*c.tensors(), out={n: t[:c.T] for n, t in out.items()})
+    assert s.check_device_error() == 0
+    for t in out.values():
+        assert bool((t[c.T:] == 9.0).all())
+    after = (c.cache.k, c.cache.v, c.cache.ts, c.cache.page_table, c.cache.lens, c.cache.ref)
+    for a, b in zip(before, after):
+        assert torch.equal(a.view(torch.int16) if a.dtype == torch.bfloat16 else a, b.view(torch.int16) if b.dtype == torch.bfloat16 else b)

@@ -216,3 +216,24 @@ def test_whole_layer_with_window():
         setattr(sub, n, s["f1"][n].cpu())
     assert_bf16(s["attn"]["y"], oracle.attn_fwd(sub), "y", storage_fwd(sub)["y"])
     assert all(torch.isfinite(t.float()).all() for t in g.values())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_rows_with_sinks_backward(d):
+    """Rows long enough that the queries of the sinks' key tile are worked in chunks (more than 512
+    tokens, 1 to 128 sinks), beside rows where they are not: one of exactly 512, one with 129 sinks,
+    one with none; dK and dV are the same bits twice."""
+    w = W.make_window([2500, 512, 513, 1100, 1300, 40, 700], [4, 3, 128, 129, 0, 5, 1], [100, 50, 64, 30, 200, 7, 0], H=2, d=d, seed=11,
+                      random_affine=True, with_grad=True)
+    _, layer, t = run_layer(w)
+    runs = [layer.backward_from_dy(t["q"], t["k"], t["v"], t["rab_pos"], t["rab_time"], t["grad"]) for _ in range(2)]
+    assert layer.check_device_error() == 0
+    ref = oracle.attn_bwd(w, oracle.f32(w.grad))
+    with oracle.bf16_operands():
+        model = oracle.attn_bwd(w, oracle.f32(w.grad))
+    for n, r, m in zip(("dq", "dk", "dv"), ref, model):
+        assert_bf16(runs[0][n], r, n, bf16(m))
+    for n, r in zip(("d_rab_pos", "d_rab_time"), ref[3:]):
+        assert errors(runs[0][n], r)[0] <= 2e-5, n
+    for n in ("dk", "dv"):
+        assert torch.equal(runs[0][n], runs[1][n])

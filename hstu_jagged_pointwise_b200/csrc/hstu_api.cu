@@ -6,6 +6,7 @@
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
+#include <algorithm>
 
 #include <atomic>
 #include <mutex>
@@ -498,6 +499,18 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
     sp.b_m = 1;
     sp.cut = kind == HSTU_KIND_WINDOW && d.dtype == HSTU_BF16;
     sp.ascending = 1;        // backward items are key tiles: the first one is seen by most queries
+    // tensor-core backward: dQ's sums and, behind them, the CTAs' parts of the bias gradients
+    // start at zero (the last 16-byte word may end in the padding that follows them)
+    int grid = 0;
+    float* dq_acc = at<float>(workspace, L.dq_acc);
+    float* rab_part = at<float>(workspace, L.rab_part);
+    if (d.dtype == HSTU_BF16) {
+        const DevInfo* di = dev_info();
+        if (!di) return HSTU_ERR_CUDA;
+        grid = di->sms < kMaxBwdCtas ? di->sms : kMaxBwdCtas;
+        sp.zero = at<uint4>(workspace, L.dq_acc);
+        sp.n_zero = (long long)((L.rab_part - L.dq_acc + (size_t)grid * (2 * d.n_pos - 1 + d.n_tbuckets) * 4 + 15) / 16);
+    }
     sp.ctrl = ctrl;
     sp.items = at<int4>(workspace, L.items);
     sp.perm = at<int>(workspace, L.perm);
@@ -564,21 +577,11 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
         p.d_rab_time = d_rab_time;
         return cuda_status(launch_attn_bwd_simt(1, d.d_qk, p, s));
     }
-    const DevInfo* di = dev_info();
-    if (!di) return HSTU_ERR_CUDA;
     CUtensorMap tq, tk, tv, tdy, tdq;
-    float* dq_acc = at<float>(workspace, L.dq_acc);
     const int dq_box_cols = d.d_qk == 128 ? 32 : 16;
     if (!make_tmap(&tq, q, d.T, D, 64) || !make_tmap(&tk, k, d.T, D) || !make_tmap(&tv, v, d.T, D) ||
         !make_tmap(&tdy, lp.dy, d.T, D, 64) || !make_tmap_f32(&tdq, dq_acc, d.T, D, dq_box_cols, kBwdEwCols))
         return HSTU_ERR_CUDA;
-    st = cuda_status(cudaMemsetAsync(dq_acc, 0, (size_t)d.T * D * sizeof(float), s));
-    if (st != HSTU_OK) return st;
-    const int grid = di->sms < kMaxBwdCtas ? di->sms : kMaxBwdCtas;
-    const int rab_w = 2 * d.n_pos - 1 + d.n_tbuckets;
-    float* rab_part = at<float>(workspace, L.rab_part);
-    st = cuda_status(cudaMemsetAsync(rab_part, 0, (size_t)grid * rab_w * sizeof(float), s));
-    if (st != HSTU_OK) return st;
     BwdParams bp;
     memset(&bp, 0, sizeof(bp));
     bp.dbg = debug_wait();
@@ -590,25 +593,27 @@ int attn_bwd_impl(const hstu_dims* dims, const hstu_mask_spec* mask, const hstu_
     bp.rab_time = rab_time;
     bp.items = sp.items;
     bp.ctrl = ctrl;
-    bp.dq_acc = dq_acc;
     bp.dk = static_cast<__nv_bfloat16*>(dk);
     bp.dv = static_cast<__nv_bfloat16*>(dv);
     bp.rab_part = rab_part;
     bp.H = d.H;
     bp.P = d.n_pos;
     bp.nb = d.n_tbuckets;
-    bp.ld = D;
     bp.inv_alpha = 1.0f / d.alpha;
     bp.sink_part = at<float>(workspace, L.sink_part);
     st = cuda_status(launch_attn_bwd_tc(kind, d.d_qk, tq, tk, tv, tdy, tdq, bp, grid, s));
     if (st != HSTU_OK) return st;
-    if (kind == HSTU_KIND_WINDOW && d.max_seq_len > kTileM * kSinkChunk) {
-        st = cuda_status(launch_sink_reduce(d.d_qk, d.B, bp, s));
-        if (st != HSTU_OK) return st;
-    }
-    st = cuda_status(launch_rab_reduce(rab_part, grid, d.n_pos, d.n_tbuckets, d_rab_pos, d_rab_time, s));
-    if (st != HSTU_OK) return st;
-    return cuda_status(launch_f32_to_bf16(dq_acc, static_cast<__nv_bfloat16*>(dq), (long long)d.T * D, s));
+    BwdFinish bf;
+    memset(&bf, 0, sizeof(bf));
+    bf.d_rab_pos = d_rab_pos;
+    bf.d_rab_time = d_rab_time;
+    bf.perm = sp.perm;
+    bf.dq_acc = dq_acc;
+    bf.dq = static_cast<__nv_bfloat16*>(dq);
+    bf.n_part = grid;
+    const int cut = kTileM * kSinkChunk;                 // longer sequences are cut: at most T / (cut + 1) of them
+    const int n_cut = sp.cut && d.max_seq_len > cut ? std::min(d.B, d.T / (cut + 1)) : 0;
+    return cuda_status(launch_bwd_finish(d.d_qk, d.T, n_cut, bp, bf, s));
 }
 
 }  // namespace

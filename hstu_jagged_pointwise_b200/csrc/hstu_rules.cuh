@@ -142,6 +142,12 @@ __device__ __forceinline__ int sink_chunks(int L, int S) {
     return S >= 1 && S <= 128 && n > 1 ? n : 1;
 }
 
+// Whether any query of chunk k sees key r of the first key tile (past the window only the sinks
+// are seen, and the chunk's sums of the other keys are neither written nor read).
+__device__ __forceinline__ bool sink_chunk_sees(int k, int r, int S, int R) {
+    return r < S || 128 * kSinkChunk * k - r < R;
+}
+
 // First place of a cut sequence's chunks in the partial sums: a sequence of more than 512
 // tokens has at most L / 512 + 1 chunks, so two places for each 512 tokens before it keep
 // the sequences apart.

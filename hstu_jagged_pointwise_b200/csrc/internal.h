@@ -58,6 +58,8 @@ struct SchedParams {
     int cut;         // window kind, bf16 backward: the sinks' key tile in chunks of kSinkChunk query tiles
     int ascending;   // causal/MTGR tile order inside a group: 1 = first tile first (backward key tiles)
     Control* ctrl;
+    uint4* zero;     // n_zero 16-byte words cleared beside the schedule (sums the caller's next kernel adds to)
+    long long n_zero;
     int4* items;
     int* perm;       // [B]
     int* seq_base;   // [B]
@@ -84,7 +86,10 @@ struct FwdParams {
     DebugWait dbg;
 };
 
-// tcgen05 backward: one work item = (sequence, head, 128-key tile).
+// tcgen05 backward: one work item = (sequence, head, 128-key tile).  Rows of q, k, v and the
+// gradients are H * d elements.  Nothing is added to these 128 bytes without timing every kind:
+// 16 more changed the register allocation (34 bytes more spilled) and cost the causal kernel 5%
+// (262144 tokens in rows of 2048, four heads of 128: 2976 -> 3142 us).
 struct BwdParams {
     const int32_t* off;
     const int64_t* ts;
@@ -94,15 +99,16 @@ struct BwdParams {
     const float* rab_time;
     const int4* items;
     Control* ctrl;
-    float* dq_acc;            // [T, H*d] fp32, zeroed before the launch (written via tm_dq)
     __nv_bfloat16* dk;
     __nv_bfloat16* dv;
     float* rab_part;          // [grid][2P-1 + nb] per-CTA rab gradient partial sums, zeroed
-    int H, P, nb, ld;
-    float inv_alpha;          // 1 / alpha (window kind, which reads dY unscaled)
     float* sink_part;         // window kind: [place][H][dK, dV][128][d] of the sinks' key tile, by chunk
+    int H, P, nb;
+    float inv_alpha;          // 1 / alpha (window kind, which reads dY unscaled)
     DebugWait dbg;
 };
+
+static_assert(sizeof(BwdParams) == 128, "see above");
 
 constexpr int kMaxBwdCtas = 1024;   // bound on the backward's persistent grid (workspace sizing)
 
@@ -204,8 +210,8 @@ cudaError_t ensure_smem_limit(const void* fn, int bytes);
 enum ProfKind {
     kProfSchedule = 0, kProfAttnFwdTc, kProfAttnFwdSimt, kProfLnFwd, kProfLnBwd, kProfLnBwdReduce,
     kProfAttnBwdDkvSimt, kProfAttnBwdDqSimt, kProfDebugIndices, kProfAttnBwdTc, kProfDqConvert,
-    kProfRabReduce, kProfCacheScan, kProfCacheCopy, kProfGemm, kProfSiluGrad, kProfColSum, kProfSlSample, kProfGather,
-    kProfScaleDy, kProfSinkReduce, kProfKinds
+    kProfCacheScan, kProfCacheCopy, kProfGemm, kProfSiluGrad, kProfColSum, kProfSlSample, kProfGather,
+    kProfScaleDy, kProfKinds
 };
 void prof_begin(int kind, cudaStream_t s);
 void prof_end(int kind, cudaStream_t s);
@@ -227,14 +233,21 @@ constexpr int kBwdEwCols = 16;
 cudaError_t launch_attn_bwd_tc(int kind, int d, const CUtensorMap& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, const CUtensorMap& tdy, const CUtensorMap& tdq,
                                const BwdParams& p, int grid, cudaStream_t s);
-// dK and dV of the first key tile of every cut sequence: the sums over its chunks, in order.
-cudaError_t launch_sink_reduce(int d, int B, const BwdParams& p, cudaStream_t s);
-cudaError_t launch_f32_to_bf16(const float* src, __nv_bfloat16* dst, long long n, cudaStream_t s);
+// After the attention: the bias gradients from the CTAs' parts, dK and dV of cut sequences
+// (the first n_cut of perm hold them all), dQ to bf16.  The counts are the launcher's.
+struct BwdFinish {
+    float *d_rab_pos, *d_rab_time;
+    const int* perm;
+    const float* dq_acc;      // [T, H*d] fp32
+    __nv_bfloat16* dq;
+    int n_part;
+    int n_rab, n_sink;
+    long long n4;
+};
+cudaError_t launch_bwd_finish(int d, long long T, int n_cut, const BwdParams& p, BwdFinish f, cudaStream_t s);
 // dst = bf16(src * scale), n a multiple of 8 (16-byte vectors)
 cudaError_t launch_scale_bf16(const __nv_bfloat16* src, __nv_bfloat16* dst, float scale, long long n,
                               cudaStream_t s);
-cudaError_t launch_rab_reduce(const float* part, int n_part, int P, int nb, float* d_rab_pos,
-                              float* d_rab_time, cudaStream_t s);
 cudaError_t launch_ln_fwd(int dtype_f32, const LnParams& p, cudaStream_t s);
 cudaError_t launch_ln_bwd(int dtype_f32, const LnParams& p, cudaStream_t s);
 int ln_bwd_partials(long long T);

@@ -30,7 +30,7 @@
 // for all nodes of a warp, so most rows of scores need one constant a key.
 //
 // One CTA = 24 warps, each with little to wait for but its own input, since a wait that ends
-// at once still costs some 200 cycles (at 128 keys x 128 nodes a tile takes about 1700):
+// at once still costs some 200 cycles (at 128 keys x 128 nodes a tile takes about 1900):
 //   0-15   elementwise and epilogue
 //   16     producer: TMA of Q and of the K and V pages
 //   17     issues the score products, up to two tiles ahead
@@ -1200,11 +1200,16 @@ struct TreeWs {
     int max_splits, min_tiles, group;
 };
 
-// Groups: 64 nodes (narrow) where no tree has more, else 128 (wide).  Parts of a history:
-// where the trees alone give at least four work items an SM, none (the sums go through HBM
-// once); else so many that there are about sixteen an SM, of at least min_tiles tiles (an
-// item's start costs about two tiles' time), which is eight where the work allows it and
-// one for a single short history.  The parts' sums stay within 32 MB, which L2 holds.
+// Groups: 64 nodes (narrow) where no tree has more, else 128 (wide).  Whole scorer, narrow / wide:
+// 64 trees of one node over 4096 events 94 / 98 us, of 16 100 / 105, of 64 122 / 125; 32 trees of 65
+// over 2048 70 / 61, of 128 70 / 63, of 512 178 / 145.
+// Parts of a history: where the trees alone give at least four work items an SM, none (the sums
+// go through HBM once); else so many that there are about sixteen an SM, of at least min_tiles
+// tiles (an item's start costs about two tiles' time), which is eight where the work allows it
+// and one for a single short history.  The parts' sums stay within 32 MB, which L2 holds.
+// One part always / this rule: one node over 2048 events 25 / 19 us; 16 trees of 1 to 4 over 100 to
+// 8192 76 / 64; 8 of 16 over 8192 69 / 39; 64 of one over 4096 to 8192 146 / 133; 48 of 5 to 60 over a
+// window of 700 39 / 40.  At least 16 tiles in place of 8: 56 / 48 us for 48 of 5 to 61 over 0 to 2048.
 TreeWs tree_ws(const hstu_tree_dims& d, const hstu_page_cache& c) {
     TreeWs w;
     w.group = d.max_nodes <= kNarrow ? kNarrow : kWide;
@@ -1212,7 +1217,7 @@ TreeWs tree_ws(const hstu_tree_dims& d, const hstu_page_cache& c) {
     const long long groups = full + d.B;                                    // at most
     const long long whole = d.H * (full > d.B ? full : (long long)d.B);     // at least, where no tree is empty
     const long long tiles = ((long long)c.max_pages * c.page_size + kTileN - 1) / kTileN;
-    long long min_tiles = whole * tiles / (148 * 4);
+    long long min_tiles = whole * tiles / (148 * 2);
     min_tiles = min_tiles < 1 ? 1 : (min_tiles > 8 ? 8 : min_tiles);
     long long splits = whole < 148 * 4 && whole > 0 ? (148 * 16 + whole - 1) / whole : 1;
     const long long by_size = (32LL << 20) / ((long long)d.T * d.H * d.d * 4 + 1);

@@ -175,6 +175,28 @@ __device__ __forceinline__ void fwd_block2(uint32_t taddr, const float* dg, cons
 }
 
 // ------------------------------------------------------------------ kernel
+// Lanes 4k .. 4k + 3 hold four 16-byte pieces each; lane 4k + a gets piece a of all four, w[b]
+// from lane 4k + b.  All lanes of the warp take part.
+__device__ __forceinline__ void quad_transpose(uint4 (&w)[4]) {
+    const unsigned lane = threadIdx.x;
+    auto swap = [&](uint4& keep0, uint4& keep1, bool hi, int x) {      // lanes x apart: keep1 of the low one for keep0 of the high one
+        uint4 send = hi ? keep0 : keep1;
+        send.x = __shfl_xor_sync(kFull, send.x, x);
+        send.y = __shfl_xor_sync(kFull, send.y, x);
+        send.z = __shfl_xor_sync(kFull, send.z, x);
+        send.w = __shfl_xor_sync(kFull, send.w, x);
+        if (hi) keep0 = send;
+        else keep1 = send;
+    };
+    swap(w[0], w[1], lane & 1, 1);
+    swap(w[2], w[3], lane & 1, 1);
+    swap(w[0], w[2], lane & 2, 2);
+    swap(w[1], w[3], lane & 2, 2);
+}
+
+// The n lowest bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32)); }
+
 template <int KIND, int D>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -534,12 +556,12 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                          (KIND != HSTU_KIND_CAUSAL && KIND != HSTU_KIND_WINDOW && r0 >= s.S + s.R);
                 // real-time / history rows against non-candidate keys: the mask is j <= i (a
                 // static key precedes every real-time row)
-                // window rows: the mask depends on j - i alone unless the block's keys are part
-                // sinks, part not
-                const bool causal_rows = KIND == HSTU_KIND_CAUSAL ||
-                                         (KIND == HSTU_KIND_WINDOW
-                                              ? n0 >= s.S || n0 + 63 < s.S
-                                              : KIND != HSTU_KIND_MFALCON && r0 >= s.S && r_hi < s.S + s.R &&
+                // window rows: the mask depends on j - i alone, except where the block's keys are part
+                // sinks, part not, or end with the row; there (odd) each lane keeps the keys that
+                // its row sees by a bit mask over P
+                const bool odd = KIND == HSTU_KIND_WINDOW && ((wcls == 1 && n0 < s.S && n0 + 63 >= s.S) || n0 + 64 > s.Lk);
+                const bool causal_rows = KIND == HSTU_KIND_CAUSAL || KIND == HSTU_KIND_WINDOW ||
+                                         (KIND != HSTU_KIND_MFALCON && r0 >= s.S && r_hi < s.S + s.R &&
                                                     n0 < s.S + s.R);
                 // keys n0 + k with k >= jlim are masked for every row of the block: static rows
                 // against a key block that crosses the end of the static segment, real-time rows
@@ -555,7 +577,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 // window rows far past a key block that crosses the end of the sinks see its
                 // sinks only (i - j >= R for the rest, and every row is past every key)
-                if (KIND == HSTU_KIND_WINDOW && wcls == 1 && !causal_rows && r0 - (n0 + 63) >= s.R) {
+                if (KIND == HSTU_KIND_WINDOW && odd && wcls == 1 && r0 - (n0 + 63) >= s.R) {
                     jlim = s.S - n0;
                     wcls = 2;
                 }
@@ -566,7 +588,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (rmin > cmax) wcls = 2;
                     else if (rmax <= cmin) wcls = 0;
                 }
-                const bool dense = wcls != 0 && n0 + 64 <= s.Lk && (wcls == 2 || causal_rows);
+                const bool dense = wcls != 0 && (KIND == HSTU_KIND_WINDOW || (n0 + 64 <= s.Lk && (wcls == 2 || causal_rows)));
                 if (dense) {
                     tc = classify_time(rmin, rmax, cmin, cmax, p.nb);
                     const int dmax = col_pos<KIND>(s, n0 + 63) - pr_lo;
@@ -594,7 +616,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             for (int k = lane; k < 95; k += 32) {
                                 const int dl = d0 + k;
                                 const bool masked = (causal_rows && dl > 0) ||
-                                                    (KIND == HSTU_KIND_WINDOW && wcls == 1 && n0 >= s.S && -dl >= s.R);
+                                                    (KIND == HSTU_KIND_WINDOW && wcls == 1 && !odd && n0 >= s.S && -dl >= s.R);
                                 const int pi = pm == kPosUniform ? pidx_u : min(max(dl, -(p.P - 1)), p.P - 1) + p.P - 1;
                                 w_diag[k] = masked ? kMaskedHalfBias : 0.5f * s_rp[pi] + tadd;
                             }
@@ -622,7 +644,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int cc = 0; cc < 2; cc++) {
                     const int c = 2 * g + cc;                // 32-column chunk of the tile
                     uint32_t pk[16];
-                    if (wcls == 0) {
+                    if (wcls == 0 || (KIND == HSTU_KIND_WINDOW && 32 * cc >= jlim)) {
                         // nothing visible (masked or past the sequence): P = 0, S is never read
 #pragma unroll
                         for (int e = 0; e < 16; e++) pk[e] = 0u;
@@ -665,7 +687,17 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     else if (pm >= 0 && tm == kTimeTwo)
                         fwd_block2<kBiasRowTwo>(sa, dg, cr, a_i, c0, s_rth, nbm1, pk, tc.thr, s_rth[tc.tb_lo], s_rth[tc.tb_hi]);
                     else fwd_block2<kBiasRowTime>(sa, dg, cr, a_i, c0, s_rth, nbm1, pk);
-                    if ((KIND == HSTU_KIND_MTGR || KIND == HSTU_KIND_MFSEQ || KIND == HSTU_KIND_WINDOW) && pm >= 0 && jlim - 32 * cc < 32) {
+                    if (KIND == HSTU_KIND_WINDOW && odd) {
+                        // bit k: key jb + k is at most i, in the row, and in the window or a sink
+                        const int jb = n0 + 32 * cc;
+                        const uint32_t keep = low_bits(min(i + 1, s.Lk) - jb) & (~low_bits(max(i - s.R + 1, 0) - jb) | low_bits(s.S - jb));
+#pragma unroll
+                        for (int e = 0; e < 16; e++) {
+                            if (!(keep & (1u << (2 * e)))) pk[e] &= 0xffff0000u;
+                            if (!(keep & (2u << (2 * e)))) pk[e] &= 0x0000ffffu;
+                        }
+                    }
+                    if ((KIND == HSTU_KIND_MTGR || KIND == HSTU_KIND_MFSEQ) && pm >= 0 && jlim - 32 * cc < 32) {
                         // keys past the block's column limit: P = 0 (bf16 pairs, key 2e in the low half)
                         const int lim = jlim - 32 * cc;
 #pragma unroll
@@ -714,11 +746,12 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_base + kOCol + 32 * c, v);
                 tmem_ld_wait(v);
-                if (row_ok) {
+                uint4 w[4];
+                {
                     float o[32];
 #pragma unroll
                     for (int e = 0; e < 32; e++) o[e] = n_done ? __uint_as_float(v[e]) : 0.f;
-                    if (KIND == HSTU_KIND_MFALCON) {
+                    if (KIND == HSTU_KIND_MFALCON && row_ok) {
                         const uint4* vs = reinterpret_cast<const uint4*>(vself + 32 * c);
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
@@ -732,15 +765,20 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             }
                         }
                     }
-                    uint4 w[4];
                     uint32_t* wp = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
                     for (int e = 0; e < 16; e++)
                         wp[e] = pack_bf16x2(o[2 * e] * p.inv_alpha, o[2 * e + 1] * p.inv_alpha);
-                    uint4* dst = reinterpret_cast<uint4*>(p.y + (size_t)(s.q0 + i) * p.ld +
-                                                          (size_t)s.h * D + 32 * c);
+                }
+                // lane l holds row l's four 16-byte pieces; after the transpose of each four lanes
+                // it holds piece l % 4 of their four rows, and a store writes 64 bytes of 8 rows
+                // where it wrote 16 of 32
+                quad_transpose(w);
+                __nv_bfloat16* dst = p.y + (size_t)(s.q0 + r0) * p.ld + (size_t)s.h * D + 32 * c + 8 * (lane & 3);
 #pragma unroll
-                    for (int e = 0; e < 4; e++) dst[e] = w[e];
+                for (int e = 0; e < 4; e++) {
+                    const int row = (lane & ~3) + e;
+                    if (r0 + row < s.row_end) *reinterpret_cast<uint4*>(dst + (size_t)row * p.ld) = w[e];
                 }
             }
             tc_fence_before();

@@ -66,11 +66,13 @@ __device__ int block_exclusive_scan(int v, int* warp_sums, int* total) {
     return r;
 }
 
-// Blocks that clear p.zero, one an SM beside the schedule's: the schedule takes one SM for 5 us,
+// Blocks that clear p.zero, one an SM beside the schedule's: the schedule takes one SM for 4 us,
 // in which the others write what two memsets took 2 x 1.5 us and more for (22000 tokens of 512,
-// schedule and memsets 4.8 + 6.8 -> 8.3 us).
+// schedule and memsets 4.8 + 6.8 -> 7.6 us).
 constexpr long long kZeroBlocks = 147;
 
+// No loop is unrolled: each runs once or twice in a batch of a thousand sequences, and what a
+// kernel this short takes is to a good part the fetch of its code (4.5 -> 4.0 us).
 __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
     __shared__ int hist[kSchedBins];
     __shared__ int warp_sums[32];
@@ -80,9 +82,11 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
     const int tid = threadIdx.x;
     if (blockIdx.x > 0) {
         const long long step = (long long)(gridDim.x - 1) * kThreads;
+#pragma unroll 1
         for (long long i = (blockIdx.x - 1LL) * kThreads + tid; i < p.n_zero; i += step) p.zero[i] = make_uint4(0, 0, 0, 0);
         return;
     }
+#pragma unroll 1
     for (int i = tid; i < kSchedBins; i += kThreads) hist[i] = 0;
     if (tid == 0) {
         p.ctrl->counter = 0;
@@ -95,6 +99,7 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
         if (p.q_off[0] != 0 || p.q_off[p.B] != p.Tq) bad = 1;
         if (p.kv_off != p.q_off && (p.kv_off[0] != 0 || p.kv_off[p.B] != p.Tkv)) bad = 1;
     }
+#pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
         const int Lq = p.q_off[b + 1] - p.q_off[b];
         if (Lq < 0 || Lq > p.max_q_len) bad = 1;
@@ -119,6 +124,7 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
     }
 
     // ---- 2. counting sort of sequences by key-tile count, longest first
+#pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
         const int Lk = p.kv_off[b + 1] - p.kv_off[b];
         const int key = min((Lk + kTileN - 1) / kTileN, kSchedBins - 1);
@@ -141,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
         }
     }
     __syncthreads();
+#pragma unroll 1
     for (int b = tid; b < p.B; b += kThreads) {
         const int Lk = p.kv_off[b + 1] - p.kv_off[b];
         const int key = min((Lk + kTileN - 1) / kTileN, kSchedBins - 1);
@@ -150,6 +157,7 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
     __syncthreads();
 
     // ---- 3. item base of every ranked sequence
+#pragma unroll 1
     for (int r0 = 0; r0 < p.B; r0 += kThreads) {
         const int r = r0 + tid;
         int nt = 0;
@@ -176,12 +184,14 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
 
     // ---- 4. items: (ranked sequence, head, tile)
     const int warp = tid >> 5, lane = tid & 31;
+#pragma unroll 1
     for (int r = warp; r < p.B; r += kThreads / 32) {
         const int b = p.perm[r];
         const int Lq = p.q_off[b + 1] - p.q_off[b];
         const int nc = p.cut ? sink_chunks(Lq, p.n_static[b]) : 1;
         const int nt = n_q_tiles(p, Lq) + nc - 1;
         const long long base = (long long)p.seq_base[r] * p.H;
+#pragma unroll 1
         for (int e = lane; e < nt * p.H; e += 32) {
             const int h = e / nt, k = e % nt;
             int row0, row_end;

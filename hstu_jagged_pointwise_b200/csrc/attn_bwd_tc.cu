@@ -854,7 +854,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                             vs * __uint_as_float(vv[e + 3]));
                         }
                     }
-                } else if (key_ok) {
+                } else {
                     uint4 wv[2], wk[2];
                     uint32_t* pv = reinterpret_cast<uint32_t*>(wv);
                     uint32_t* pk = reinterpret_cast<uint32_t*>(wk);
@@ -864,13 +864,19 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         pv[e] = n_done ? pack_bf16x2(vs * __uint_as_float(vv[2 * e]), vs * __uint_as_float(vv[2 * e + 1])) : 0u;
                         pk[e] = n_done ? pack_bf16x2(__uint_as_float(kv[2 * e]), __uint_as_float(kv[2 * e + 1])) : 0u;
                     }
-                    const size_t o = (size_t)(s.off0 + j) * p.H * D + (size_t)s.h * D + col;
-                    uint4* dv = reinterpret_cast<uint4*>(p.dv + o);
-                    uint4* dk = reinterpret_cast<uint4*>(p.dk + o);
-                    dv[0] = wv[0];
-                    dv[1] = wv[1];
-                    dk[0] = wk[0];
-                    dk[1] = wk[1];
+                    // two lanes exchange pieces, so that a store writes 32 bytes of 16 rows and not 16
+                    // of 32 (causal backward, 262144 tokens of four heads: 3297 -> 3202 us)
+                    swap_pieces(wv[0], wv[1], 1);
+                    swap_pieces(wk[0], wk[1], 1);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int jr = s.n0 + (r & ~1) + e;
+                        if (jr < s.n_end) {
+                            const size_t o = (size_t)(s.off0 + jr) * p.H * D + (size_t)s.h * D + col + 8 * (lane & 1);
+                            *reinterpret_cast<uint4*>(p.dv + o) = wv[e];
+                            *reinterpret_cast<uint4*>(p.dk + o) = wk[e];
+                        }
+                    }
                 }
             }
             tc_fence_before();

@@ -175,25 +175,6 @@ __device__ __forceinline__ void fwd_block2(uint32_t taddr, const float* dg, cons
 }
 
 // ------------------------------------------------------------------ kernel
-// Lanes 4k .. 4k + 3 hold four 16-byte pieces each; lane 4k + a gets piece a of all four, w[b]
-// from lane 4k + b.  All lanes of the warp take part.
-__device__ __forceinline__ void quad_transpose(uint4 (&w)[4]) {
-    const unsigned lane = threadIdx.x;
-    auto swap = [&](uint4& keep0, uint4& keep1, bool hi, int x) {      // lanes x apart: keep1 of the low one for keep0 of the high one
-        uint4 send = hi ? keep0 : keep1;
-        send.x = __shfl_xor_sync(kFull, send.x, x);
-        send.y = __shfl_xor_sync(kFull, send.y, x);
-        send.z = __shfl_xor_sync(kFull, send.z, x);
-        send.w = __shfl_xor_sync(kFull, send.w, x);
-        if (hi) keep0 = send;
-        else keep1 = send;
-    };
-    swap(w[0], w[1], lane & 1, 1);
-    swap(w[2], w[3], lane & 1, 1);
-    swap(w[0], w[2], lane & 2, 2);
-    swap(w[1], w[3], lane & 2, 2);
-}
-
 // The n lowest bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32)); }
 

@@ -67,4 +67,25 @@ __device__ __forceinline__ int time_bucket_u32(uint32_t x, int nbm1) {
     return min(32 - __clz((int)x), nbm1);
 }
 
+// Lanes `x` apart swap: the low one's b for the high one's a.  All lanes of the warp take part.
+__device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, int x) {
+    const bool hi = threadIdx.x & x;
+    uint4 send = hi ? a : b;
+    send.x = __shfl_xor_sync(0xffffffffu, send.x, x);
+    send.y = __shfl_xor_sync(0xffffffffu, send.y, x);
+    send.z = __shfl_xor_sync(0xffffffffu, send.z, x);
+    send.w = __shfl_xor_sync(0xffffffffu, send.w, x);
+    if (hi) a = send;
+    else b = send;
+}
+
+// Lanes 4k .. 4k + 3 hold four 16-byte pieces each; lane 4k + a gets piece a of all four, w[b]
+// from lane 4k + b.
+__device__ __forceinline__ void quad_transpose(uint4 (&w)[4]) {
+    swap_pieces(w[0], w[1], 1);
+    swap_pieces(w[2], w[3], 1);
+    swap_pieces(w[0], w[2], 2);
+    swap_pieces(w[1], w[3], 2);
+}
+
 }  // namespace hstu

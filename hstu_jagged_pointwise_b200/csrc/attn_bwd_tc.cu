@@ -667,16 +667,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     TimeClass tc;
                     tc.tb_lo = tc.tb_hi = 0;
                     tc.thr = 0;
-                    // window: keys part sinks, part not.  Queries far past such a block see its sinks
-                    // only: the other lanes are switched off (lane_off)
-                    const bool mixed = KIND == HSTU_KIND_WINDOW && ka < s.S && s.S <= ka + 31;
-                    bool lane_off = false;
-                    if (mixed && wcls == 1 && i0 - (ka + 31) >= s.R) {
-                        lane_off = j >= s.S;
-                        wcls = 2;
-                    }
-                    const bool dense = wcls != 0 && warp_keys == 32 && i0 + C <= s.L &&
-                                       (KIND == HSTU_KIND_CAUSAL || wcls == 2 || (KIND == HSTU_KIND_WINDOW && !mixed));
+                    // window: a block whose keys are part sinks, part not, or which the row's end cuts
+                    // (odd): each key keeps the queries that see it by a bit mask.  Queries far past
+                    // a mixed block see its sinks only.
+                    const bool odd = KIND == HSTU_KIND_WINDOW && wcls != 0 &&
+                                     ((wcls == 1 && ka < s.S && s.S <= ka + 31) || warp_keys < 32 || i0 + C > s.L);
+                    if (odd && wcls == 1 && i0 - (ka + 31) >= s.R && ka < s.S) wcls = 2;
+                    const bool dense = wcls != 0 && (KIND == HSTU_KIND_WINDOW || (warp_keys == 32 && i0 + C <= s.L &&
+                                                     (KIND == HSTU_KIND_CAUSAL || wcls == 2)));
                     const int dmin = ka - (i0 + C - 1);  // smallest key - query of the block
                     if (dense) {
                         tc = classify_time(kmin, kmax, qmin, qmax, p.nb);
@@ -693,7 +691,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             else for (int k = lane; k < C + 31; k += 32) {
                                 const int dl = dmin + k;
                                 const bool masked = (KIND == HSTU_KIND_CAUSAL && dl > 0) ||
-                                                    (KIND == HSTU_KIND_WINDOW && wcls == 1 && (dl > 0 || (ka >= s.S && -dl >= s.R)));
+                                                    (KIND == HSTU_KIND_WINDOW && wcls == 1 && !odd && (dl > 0 || (ka >= s.S && -dl >= s.R)));
                                 w_diag[k] = masked ? kMaskedHalfBias
                                                    : 0.5f * s_rp[min(max(dl, -(p.P - 1)), p.P - 1) + p.P - 1] + tadd;
                             }
@@ -720,9 +718,14 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tmem_ld_wait(dp);
                         const float* dg = w_diag + lane + C - 1;
                         constexpr bool X = KIND == HSTU_KIND_WINDOW;
-                        if (X && lane_off) {
+                        uint32_t keep = 0;
+                        if (X && odd) {
+                            // bit e: query i0 + e is at least j, in the row, and within the window of a key that
+                            // is no sink; dz = 0 and P = 0 elsewhere, whatever lies there
+                            if (key_ok) keep = low_bits((j < s.S || s.R >= s.L ? s.L : min(s.L, j + s.R)) - i0) & ~low_bits(j - i0);
 #pragma unroll
-                            for (int e = 0; e < C; e++) dp[e] = 0u;          // dz = 0: no gradient from this key
+                            for (int e = 0; e < C; e++)
+                                if (!(keep & (1u << e))) sv[e] = dp[e] = 0u;
                         }
                         if (pm == kPosUniform && tm == kTimeUniform)
                             bwd_block<false, C, X, true>(sv, dp, dg, c0, false, dlo, dhi, w_qrel, a_j, s_rth, nbm1, acc, g_rt, pa, pz, p.inv_alpha);
@@ -780,9 +783,10 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             if (cur_t >= 0 && acc_t != 0.f) red_add_f32(&g_rt[cur_t], acc_t);
                             if (KIND == HSTU_KIND_CAUSAL) diag_sums<C>(zf, dlo, dhi);
                         }
-                        if (X && lane_off) {
+                        if (X && odd) {
 #pragma unroll
-                            for (int e = 0; e < C / 2; e++) pa[e] = 0u;
+                            for (int e = 0; e < C; e++)
+                                if (!(keep & (1u << e))) pa[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
                         }
                     }
                     // A^T_h back into TMEM inside the S^T_h columns this warp has read

@@ -175,9 +175,6 @@ __device__ __forceinline__ void fwd_block2(uint32_t taddr, const float* dg, cons
 }
 
 // ------------------------------------------------------------------ kernel
-// The n lowest bits (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32)); }
-
 template <int KIND, int D>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

@@ -67,6 +67,9 @@ __device__ __forceinline__ int time_bucket_u32(uint32_t x, int nbm1) {
     return min(32 - __clz((int)x), nbm1);
 }
 
+// The n lowest bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32)); }
+
 // Lanes `x` apart swap: the low one's b for the high one's a.  All lanes of the warp take part.
 __device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, int x) {
     const bool hi = threadIdx.x & x;

@@ -608,8 +608,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         if (WIDE) mma_ts_if(one, tm + kOCol, tm + kSCols * buf + 32 * (kk >> 1) + 8 * (kk & 1), dV + (kk * 2048 >> 4), kIdO, acc);
                         else mma_ss_if(one, tm + kOCol, dV + (kk * 2048 >> 4), dP + (kk * 2048 >> 4), kIdO, acc);
                     }
-                    tc_commit_if(one, &bars[kPFree0 + buf]);
                     tc_commit_if(one, &bars[kEmpty0 + at.slot]);
+                    tc_commit_if(one, &bars[kPFree0 + buf]);
                     if (v + 1 == m) tc_commit_if(one, &bars[kOFull]);
                 }
             }
@@ -713,7 +713,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     // V rows that are not live become zeros: P is zero there, but 0 * NaN is not.
                     Ring at_v = ring;
                     at_v.skip(ring_of_v(v - s.v0, s.v1 - s.v0), kSlots);
-                    ok = __all_sync(kAll, mbar_wait(&bars[kFull0 + at_v.slot], at_v.phase, s_abort, p.dbg.limit));
+                    // This warp runs ahead of the products, so the slot may still hold (or be about to
+                    // receive) the tile before: first that one's release, then this one's arrival.  A
+                    // phase alone cannot tell the tile before from this one.  (The release before that
+                    // has come: P of the tile two before, which this warp has waited for, comes after
+                    // the products of the tile four before; and this tile's own waits for this warp.)
+                    ok = __all_sync(kAll, mbar_wait(&bars[kEmpty0 + at_v.slot], at_v.phase ^ 1, s_abort, p.dbg.limit) &&
+                                              mbar_wait(&bars[kFull0 + at_v.slot], at_v.phase, s_abort, p.dbg.limit));
                     if (!ok) break;
                     if (dead) {
                         const uint32_t row = smem_u32(sm + L::ring) + at_v.slot * L::kTileBytes + r * 128;

@@ -95,7 +95,8 @@ typedef enum { HSTU_MASK_CAUSAL = 0, HSTU_MASK_MTGR = 1, HSTU_MASK_MFALCON_SEQ =
  * the window W_b of row b, each >= 0 and either may exceed the row's length (a
  * negative one sets the device status word like a bad segment size).  A row's
  * keys and values must be finite: a masked NaN or infinity inside a 128-token
- * tile that the row sees part of reaches its sum, as with the other masks.  Both pointers
+ * tile that the row sees part of reaches its sum, as with the other masks, and so does
+ * one in the first tokens of the next row, which share the row's last tile.  Both pointers
  * are ignored for HSTU_MASK_CAUSAL.  Segment sizes outside [0, L_b] set the
  * device status word (HSTU_ERR_DEVICE_BOUNDS) and the launch writes nothing. */
 typedef struct {

@@ -660,9 +660,11 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const uint32_t sa = tmem + lane_base + kSCol + 32 * c;
                     const float* dg = w_diag + 31 - (KIND != HSTU_KIND_CAUSAL && pm == kPosCol ? 0 : lane) + 32 * cc;
                     const int32_t* cr = w_crel + 32 * cc;
+                    // (window rows' blocks change kind from tile to tile, and a fourth variant costs them more
+                    // in instruction fetches than it saves: 64 rows of 16 to 776 84.5 -> 78 us without it)
                     if (pm == kPosUniform && tm == kTimeUniform) fwd_block2<kBiasConst>(sa, dg, cr, a_i, c0, s_rth, nbm1, pk);
                     else if (pm >= 0 && tm == kTimeUniform) fwd_block2<kBiasRow>(sa, dg, cr, a_i, c0, s_rth, nbm1, pk);
-                    else if (pm >= 0 && tm == kTimeTwo)
+                    else if (KIND != HSTU_KIND_WINDOW && pm >= 0 && tm == kTimeTwo)
                         fwd_block2<kBiasRowTwo>(sa, dg, cr, a_i, c0, s_rth, nbm1, pk, tc.thr, s_rth[tc.tb_lo], s_rth[tc.tb_hi]);
                     else fwd_block2<kBiasRowTime>(sa, dg, cr, a_i, c0, s_rth, nbm1, pk);
                     if (KIND == HSTU_KIND_WINDOW && odd) {

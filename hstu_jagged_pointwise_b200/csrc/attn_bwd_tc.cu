@@ -320,6 +320,7 @@ attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
+    wait_for_prior_launch();                        // the work list, dY, cleared sums
 
     if (warp == kProducerWarp) {
         // ============================================================ producer
@@ -906,9 +907,9 @@ cudaError_t launch_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
     cudaError_t e = ensure_smem_limit((const void*)attn_bwd_tc_kernel<KIND, D>, BwdSmem<D>::alloc(kMaxPos));
     if (e != cudaSuccess) return e;
     prof_begin(kProfAttnBwdTc, s);
-    attn_bwd_tc_kernel<KIND, D><<<grid, kThreads, BwdSmem<D>::alloc(p.P), s>>>(tq, tk, tv, tdy, tdq, p);
+    e = launch_early(attn_bwd_tc_kernel<KIND, D>, dim3(grid), kThreads, BwdSmem<D>::alloc(p.P), s, tq, tk, tv, tdy, tdq, p);
     prof_end(kProfAttnBwdTc, s);
-    return cudaGetLastError();
+    return e;
 }
 
 __global__ void scale_bf16_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, float scale,
@@ -942,6 +943,7 @@ template <int D>
 __global__ void __launch_bounds__(256) bwd_finish_kernel(BwdParams p, BwdFinish f) {
     const int tid = threadIdx.x;
     int blk = blockIdx.x;
+    wait_for_prior_launch();
     if (blk < f.n_rab) {
         __shared__ float s_part[kRabRows][kRabCols];
         const int w = 2 * p.P - 1 + p.nb;
@@ -1013,10 +1015,10 @@ cudaError_t launch_bwd_finish(int d, long long T, int n_cut, const BwdParams& p,
     if (blocks > 148 * 16) blocks = 148 * 16;
     const unsigned grid = (unsigned)(f.n_rab + f.n_sink + blocks);
     prof_begin(kProfDqConvert, s);
-    if (d == 128) bwd_finish_kernel<128><<<grid, 256, 0, s>>>(p, f);
-    else bwd_finish_kernel<64><<<grid, 256, 0, s>>>(p, f);
+    const cudaError_t e = d == 128 ? launch_early(bwd_finish_kernel<128>, dim3(grid), 256, 0, s, p, f)
+                                   : launch_early(bwd_finish_kernel<64>, dim3(grid), 256, 0, s, p, f);
     prof_end(kProfDqConvert, s);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_attn_bwd_tc(int kind, int d, const CUtensorMap& tq, const CUtensorMap& tk,

@@ -240,6 +240,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
+    wait_for_prior_launch();                        // the work list
 
     if (warp == kProducerWarp) {
         // ============================================================ producer
@@ -783,9 +784,9 @@ cudaError_t launch_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
     cudaError_t e = ensure_smem_limit((const void*)attn_fwd_tc_kernel<KIND, D>, FwdSmem<D>::alloc(kMaxPos));
     if (e != cudaSuccess) return e;
     prof_begin(kProfAttnFwdTc, s);
-    attn_fwd_tc_kernel<KIND, D><<<grid, kThreads, smem, s>>>(tq, tk, tv, p);
+    e = launch_early(attn_fwd_tc_kernel<KIND, D>, dim3(grid), kThreads, smem, s, tq, tk, tv, p);
     prof_end(kProfAttnFwdTc, s);
-    return cudaGetLastError();
+    return e;
 }
 
 template <int KIND, int D>

@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_window_kernel(SimtPara
     float* s_rt = s_rp + 2 * kMaxPos;
 
     const int b = blockIdx.z, h = blockIdx.y, row0 = blockIdx.x * kWM;
+    wait_for_prior_launch();
     if (!p.ctrl->valid) return;
     const SeqCtx c = seq_ctx(p, b);
     if (row0 >= c.L) return;
@@ -284,9 +285,9 @@ cudaError_t fwd_window_one(const SimtParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     dim3 grid((p.max_len + kWM - 1) / kWM, p.H, p.B);
     prof_begin(kProfAttnFwdSimt, s);
-    attn_fwd_simt_window_kernel<D><<<grid, kThreads, WinSmem<D>::bytes, s>>>(p);
+    e = launch_early(attn_fwd_simt_window_kernel<D>, grid, kThreads, WinSmem<D>::bytes, s, p);
     prof_end(kProfAttnFwdSimt, s);
-    return cudaGetLastError();
+    return e;
 }
 
 // One (query tile, key tile) block of the backward: fills sA = mask*SiLU(z)/alpha and

@@ -28,27 +28,4 @@ inline int check_cache(const hstu_page_cache* c) {
 
 DebugWait cache_debug_wait();
 
-#ifdef __CUDACC__
-// The launch before this one has completed, and its writes are visible.
-__device__ __forceinline__ void wait_for_prior_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The next launch may start: it waits by wait_for_prior_launch before it reads our results.
-__device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// Launch that may start while the one before it in the stream ends.
-template <typename... Args>
-cudaError_t launch_early(void (*kernel)(Args...), int grid, int block, uint32_t smem, cudaStream_t s, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-#endif
-
 }  // namespace hstu

@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(32 * WPR) ln_fwd_kernel(LnParams p) {
             }
         }
     };
+    wait_for_prior_launch();
     fetch(blockIdx.x);
     for (long long row = blockIdx.x; row < p.T; row += gridDim.x) {
         const size_t base = (size_t)row * p.D;
@@ -513,6 +514,16 @@ bool pick_shape(int D, int* wpr, int* ncw) {
         else KERNEL<T, 4, 8><<<GRID, 128, 0, s>>>(p);                                        \
     } while (0)
 
+#define HSTU_LN_FWD_DISPATCH(GRID, WPR_, NCW_)                                                    \
+    do {                                                                                          \
+        if (WPR_ == 1) err = launch_early(ln_fwd_kernel<T, 1, 1>, dim3(GRID), 32, 0, s, p);       \
+        else if (WPR_ == 2) err = launch_early(ln_fwd_kernel<T, 2, 1>, dim3(GRID), 64, 0, s, p);  \
+        else if (NCW_ == 1) err = launch_early(ln_fwd_kernel<T, 4, 1>, dim3(GRID), 128, 0, s, p); \
+        else if (NCW_ == 2) err = launch_early(ln_fwd_kernel<T, 4, 2>, dim3(GRID), 128, 0, s, p); \
+        else if (NCW_ == 4) err = launch_early(ln_fwd_kernel<T, 4, 4>, dim3(GRID), 128, 0, s, p); \
+        else err = launch_early(ln_fwd_kernel<T, 4, 8>, dim3(GRID), 128, 0, s, p);                \
+    } while (0)
+
 #define HSTU_GLN_DISPATCH(KERNEL, GRID, WPR_, NCW_) HSTU_LN_DISPATCH(KERNEL, GRID, WPR_, NCW_)
 
 bool grouped(const LnParams& p) { return p.G > 1; }
@@ -526,7 +537,9 @@ cudaError_t fwd_t(const LnParams& p, cudaStream_t s) {
         HSTU_GLN_DISPATCH(gln_fwd_kernel, (unsigned)p.n_part, wpr, ncw);
     } else {
         const unsigned grid = (unsigned)(p.T < kLnMaxBlocks ? p.T : kLnMaxBlocks);
-        HSTU_LN_DISPATCH(ln_fwd_kernel, grid, wpr, ncw);
+        cudaError_t err = cudaSuccess;
+        HSTU_LN_FWD_DISPATCH(grid, wpr, ncw);
+        if (err != cudaSuccess) return err;
     }
     prof_end(kProfLnFwd, s);
     return cudaGetLastError();
@@ -552,6 +565,7 @@ cudaError_t bwd_t(const LnParams& p, cudaStream_t s) {
 }
 
 #undef HSTU_LN_DISPATCH
+#undef HSTU_LN_FWD_DISPATCH
 #undef HSTU_GLN_DISPATCH
 
 }  // namespace

@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(SchedParams p) {
     __shared__ int s_carry;
 
     const int tid = threadIdx.x;
+    allow_next_launch();
     if (blockIdx.x > 0) {
         const long long step = (long long)(gridDim.x - 1) * kThreads;
 #pragma unroll 1

@@ -237,3 +237,55 @@ def test_long_rows_with_sinks_backward(d):
         assert errors(runs[0][n], r)[0] <= 2e-5, n
     for n in ("dk", "dv"):
         assert torch.equal(runs[0][n], runs[1][n])
+
+
+def test_two_layers_on_two_streams_and_replayed():
+    """Two layers' forward and backward called in turn on two streams, and as two graphs replayed side by
+    side, many times with nothing waited for between: each has what it has alone (dQ and the bias
+    gradients up to the order of their sums), and the next call in a stream sees the one before done."""
+    from hstu_jagged_pointwise_b200 import ops
+    cases = [W.make_window([1500, 700, 33, 1], [4, 0, 2, 1], [100, 64, 50, 3], H=2, d=128, seed=5, random_affine=True, with_grad=True),
+             W.make_window([900, 5, 513], [1, 3, 130], [40, 2, 300], H=3, d=64, seed=6, random_affine=True, with_grad=True)]
+    work, want = [], []
+    for w in cases:
+        fwd, layer, t = run_layer(w)
+        args = [t[n] for n in ("q", "k", "v", "u", "rab_pos", "rab_time", "gamma", "beta")]
+
+        def call(layer=layer, t=t, args=args):
+            o = dict(layer.forward(*args))
+            o.update(layer.backward(*args, o, t["grad"]))
+            return o
+        work.append(call)
+        want.append({k: v.clone() for k, v in call().items()})
+    torch.cuda.synchronize()
+    exact = ("y", "o_pre", "dk", "dv", "du")
+
+    def check(got):
+        for o, ref in zip(got, want):
+            for n, x in ref.items():
+                if n in exact:
+                    assert torch.equal(o[n], x), n
+                else:
+                    assert errors(o[n], x.double().cpu().numpy())[0] <= 1e-2, n
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [None, None]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = work[i]()
+    torch.cuda.synchronize()
+    check(got)
+    graphs, outs = [], []
+    for i, s in enumerate(streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(work[i]())
+        graphs.append(g)
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    check(outs)

@@ -158,7 +158,7 @@ Layout attn_layout(const hstu_dims& d, int is_bwd, bool window, int n_groups = 1
     size_t off = sizeof(Control);
     L.max_items = (long long)d.H * (((long long)d.T + kTileM - 1) / kTileM + d.B);
     // the window backward cuts the sinks' key tile of sequences longer than a chunk
-    const bool cut = window && is_bwd && d.dtype == HSTU_BF16;
+    const bool cut = window && is_bwd && d.dtype == HSTU_BF16 && d.max_seq_len > kTileM * kSinkChunk;
     const long long sink_places = cut ? 2 * ((long long)d.T / (kTileM * kSinkChunk) + 1) : 0;
     L.max_items += d.H * sink_places;
     L.items = off;

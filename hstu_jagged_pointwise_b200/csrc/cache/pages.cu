@@ -114,16 +114,18 @@ __device__ __forceinline__ void unclaim_slot(const PlanParams& p, int s) {
 
 constexpr int kCluster = 8;
 
-// Whether any CTA of the cluster has seen something bad.
-__device__ bool cluster_any(int bad) {
-    __shared__ int s_bad[kCluster];
+// Whether any CTA of the cluster has seen something bad; `round` counts the calls of a kernel.  Each
+// CTA writes to the others' shared memory, so every CTA must have started (a barrier of the cluster
+// comes before the first call); after the barrier here no CTA writes any more, and any may leave.
+__device__ bool cluster_any(int bad, int round) {
+    __shared__ int s_bad[2][kCluster];
     namespace cg = cooperative_groups;
     cg::cluster_group cl = cg::this_cluster();
     bad = __syncthreads_or(bad);
-    if (threadIdx.x < kCluster) *cl.map_shared_rank(&s_bad[cl.block_rank()], threadIdx.x) = bad;
+    if (threadIdx.x < kCluster) *cl.map_shared_rank(&s_bad[round][cl.block_rank()], threadIdx.x) = bad;
     cl.sync();
     int any = 0;
-    for (int i = 0; i < kCluster; i++) any |= s_bad[i];
+    for (int i = 0; i < kCluster; i++) any |= s_bad[round][i];
     return any != 0;
 }
 
@@ -261,10 +263,11 @@ constexpr int kClusterThreads = kCluster * kPlanThreads;
 __device__ __forceinline__ int cluster_thread() { return blockIdx.x * kPlanThreads + threadIdx.x; }
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) fork_kernel(PlanParams p) {
+    cooperative_groups::this_cluster().sync();        // every CTA has started
     int bad = 0, n;
     for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads)
         if (!claim_slot(p, p.slots[q], &n) || n != 0) bad = 1;
-    bool any = cluster_any(bad);                      // all slots are named
+    bool any = cluster_any(bad, 0);                   // all slots are named
     bad = 0;
     for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) {
         const int a = p.src_slots[q];
@@ -275,10 +278,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
             if (n < 0 || n > p.c.max_pages * p.c.page_size) bad = 1;
         }
     }
-    cooperative_groups::this_cluster().sync();        // the flags of the round before are read
-    any = cluster_any(bad) || any;
+    any = cluster_any(bad, 1) || any;
     for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) unclaim_slot(p, p.slots[q]);
-    cooperative_groups::this_cluster().sync();        // no CTA leaves while another may write to it
     if (any) {
         if (blockIdx.x == 0) refuse(p, kStatusBounds);
         return;
@@ -316,12 +317,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 }
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) free_kernel(PlanParams p) {
+    cooperative_groups::this_cluster().sync();        // every CTA has started
     int bad = 0, n;
     for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads)
         if (!claim_slot(p, p.slots[q], &n)) bad = 1;
-    const bool any = cluster_any(bad);
+    const bool any = cluster_any(bad, 0);
     for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) unclaim_slot(p, p.slots[q]);
-    cooperative_groups::this_cluster().sync();        // no CTA leaves while another may write to it
     if (any) {
         if (blockIdx.x == 0) refuse(p, kStatusBounds);
         return;

@@ -40,7 +40,7 @@ PageWs page_ws(const hstu_page_cache& c) {
         off = align_up(off + bytes, 256);
         return at;
     };
-    w.claim = take((size_t)c.n_slots * 4);       // 1 while a request names the slot, 0 between calls
+    w.claim = take((size_t)c.n_slots * 4);       // 1 where a request names the slot, of the slots that this call looks at
     w.base = take((size_t)c.n_slots * 4);        // request: its first place in the free list
     w.old_len = take((size_t)c.n_slots * 4);     // request: rows the slot held
     w.cow = take((size_t)c.n_slots * 4);         // request: the shared page to copy, or -1
@@ -96,8 +96,13 @@ __device__ __forceinline__ int block_exclusive(int v, int* s_warp, int* total) {
 
 __device__ __forceinline__ int pages_of(int rows, int ps) { return (rows + ps - 1) / ps; }
 
-// Names the slot of request q in claim, which is all zero between calls; false when the
-// slot is out of range, named before, or of a length that the cache cannot hold.
+// Whatever lies in claim (the workspace may have served another cache, or the scorer), a call first
+// clears the entries that it will look at.
+__device__ __forceinline__ void clear_claim(const PlanParams& p, int s) {
+    if (s >= 0 && s < p.c.n_slots) p.claim[s] = 0;
+}
+
+// Names a slot; false when it is out of range, named before, or of a length that the cache cannot hold.
 __device__ __forceinline__ bool claim_slot(const PlanParams& p, int s, int* len) {
     *len = 0;
     if (s < 0 || s >= p.c.n_slots) return false;
@@ -106,10 +111,6 @@ __device__ __forceinline__ bool claim_slot(const PlanParams& p, int s, int* len)
     if (before != 0 || n < 0 || n > p.c.max_pages * p.c.page_size) return false;
     *len = n;
     return true;
-}
-
-__device__ __forceinline__ void unclaim_slot(const PlanParams& p, int s) {
-    if (s >= 0 && s < p.c.n_slots) p.claim[s] = 0;
 }
 
 constexpr int kCluster = 8;
@@ -167,6 +168,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(PlanParams p) {
     __shared__ int s_total;
     allow_next_launch();
     const int tid = threadIdx.x, ps = p.c.page_size;
+    for (int q = tid; q < p.n_req; q += kPlanThreads) clear_claim(p, p.slots[q]);
+    __syncthreads();
     int bad = 0;
     if (tid == 0 && (p.off[0] != 0 || p.off[p.n_req] != p.T)) bad = 1;
     // pages each request needs, and its place in the list of free pages
@@ -202,9 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(PlanParams p) {
         carry += s_total;
         __syncthreads();
     }
-    bad = __syncthreads_or(bad);
-    for (int q = tid; q < p.n_req; q += kPlanThreads) unclaim_slot(p, p.slots[q]);
-    if (bad) return refuse(p, kStatusBounds);
+    if (__syncthreads_or(bad)) return refuse(p, kStatusBounds);
     if (!find_free(p, carry, s_warp, &s_total)) return refuse(p, kStatusFull);
     // nothing was changed so far; a warp takes four requests at a time from here, so that their
     // lookups are in flight together
@@ -263,7 +264,11 @@ constexpr int kClusterThreads = kCluster * kPlanThreads;
 __device__ __forceinline__ int cluster_thread() { return blockIdx.x * kPlanThreads + threadIdx.x; }
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) fork_kernel(PlanParams p) {
-    cooperative_groups::this_cluster().sync();        // every CTA has started
+    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) {
+        clear_claim(p, p.slots[q]);
+        clear_claim(p, p.src_slots[q]);
+    }
+    cooperative_groups::this_cluster().sync();        // every CTA has started, and the claims are clear
     int bad = 0, n;
     for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads)
         if (!claim_slot(p, p.slots[q], &n) || n != 0) bad = 1;
@@ -279,7 +284,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         }
     }
     any = cluster_any(bad, 1) || any;
-    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) unclaim_slot(p, p.slots[q]);
     if (any) {
         if (blockIdx.x == 0) refuse(p, kStatusBounds);
         return;
@@ -317,12 +321,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 }
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) free_kernel(PlanParams p) {
-    cooperative_groups::this_cluster().sync();        // every CTA has started
+    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) clear_claim(p, p.slots[q]);
+    cooperative_groups::this_cluster().sync();        // every CTA has started, and the claims are clear
     int bad = 0, n;
     for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads)
         if (!claim_slot(p, p.slots[q], &n)) bad = 1;
     const bool any = cluster_any(bad, 0);
-    for (int q = cluster_thread(); q < p.n_req; q += kClusterThreads) unclaim_slot(p, p.slots[q]);
     if (any) {
         if (blockIdx.x == 0) refuse(p, kStatusBounds);
         return;

@@ -57,10 +57,12 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kPrepThreads = 256;
 constexpr int kNarrow = 64, kWide = 128;   // nodes of a group in the two forms
 
-// Control block: n_items and counter of tree_attn's work list, valid = -1 after a bad tree
-// or a timeout, pad[0] CTAs of tree_attn that are done, pad[1] = valid for tree_finish.  The
-// last CTA of tree_attn sets pad[1] and clears the others for the next call.
-constexpr int kDone = 0, kVerdict = 1;
+// The scorer's words of the control block: items of tree_attn's work list and how many are taken,
+// kBad = -1 after a bad tree or a timeout, CTAs of tree_attn that are done, kVerdict = kBad for
+// tree_finish.  The last CTA of tree_attn sets kVerdict and clears the others for the next call.
+// They lie in `pad`, which nothing else writes, so that a workspace may serve the page operators
+// (which leave valid = 1) and the scorer in turn.
+enum { kItems = 0, kTaken = 1, kBad = 2, kDone = 3, kVerdict = 4 };
 
 // What tree_prep leaves for a tree: its nodes [off, off + m), history length n, live
 // history rows [0, s) and [lo, n), live 128-row tiles [0, ts) and [w0, ceil(n / 128)),
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeParams p) {
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
             atomicOr(&p.ctrl->status, kStatusBounds);
-            atomicExch(&p.ctrl->valid, -1);
+            atomicExch(&p.ctrl->pad[kBad], -1);
         }
         return;
     }
@@ -206,10 +208,10 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeParams p) {
     const int cnt = p.H * groups * t.splits;
     if (tid == 0) {
         p.info[b] = t;
-        int base = bad ? 0 : atomicAdd(&p.ctrl->n_items, cnt);
+        int base = bad ? 0 : atomicAdd(&p.ctrl->pad[kItems], cnt);
         if (bad || (long long)base + cnt > p.max_items) {
             atomicOr(&p.ctrl->status, kStatusBounds);
-            atomicExch(&p.ctrl->valid, -1);
+            atomicExch(&p.ctrl->pad[kBad], -1);
             base = -1;
         }
         s_base = base;
@@ -276,7 +278,7 @@ constexpr uint32_t kPanel = 128u * 128u;                     // 128 rows x 128 B
 __device__ __forceinline__ void flag_timeout(const TreeParams& p, volatile int* abort_flag) {
     *abort_flag = 1;
     atomicOr(&p.ctrl->status, kStatusTimeout);
-    atomicExch(&p.ctrl->valid, -1);
+    atomicExch(&p.ctrl->pad[kBad], -1);
 }
 
 struct Item {
@@ -456,13 +458,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     if (warp == kFetchWarp) {
         // ============================================================ work fetch
-        const int n_items = p.ctrl->valid == 0 ? p.ctrl->n_items : 0;
+        const int n_items = p.ctrl->pad[kBad] == 0 ? p.ctrl->pad[kItems] : 0;
         bool ok = true;
         for (int it_use = 0;; it_use++) {
             const int slot = it_use & 1;
             int idx = blockIdx.x;                           // the first item by position, the others by demand
             if (it_use > 0) {
-                if (lane == 0) idx = atomicAdd(&p.ctrl->counter, 1) + gridDim.x;
+                if (lane == 0) idx = atomicAdd(&p.ctrl->pad[kTaken], 1) + gridDim.x;
                 idx = __shfl_sync(kAll, idx, 0);
             }
             Item s;
@@ -1012,8 +1014,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         __threadfence();
         if (atomicAdd(&p.ctrl->pad[kDone], 1) == (int)gridDim.x - 1) {
             __threadfence();
-            p.ctrl->pad[kVerdict] = atomicAdd(&p.ctrl->valid, 0);
-            p.ctrl->n_items = p.ctrl->counter = p.ctrl->valid = p.ctrl->pad[kDone] = 0;
+            p.ctrl->pad[kVerdict] = atomicAdd(&p.ctrl->pad[kBad], 0);
+            p.ctrl->pad[kItems] = p.ctrl->pad[kTaken] = p.ctrl->pad[kBad] = p.ctrl->pad[kDone] = 0;
         }
     }
 }

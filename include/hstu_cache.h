@@ -16,9 +16,11 @@
  * argument errors returned before any launch.  What only the device can see is
  * recorded in the status word of `workspace` (read and cleared by
  * hstu_cache_check_device_error); the call then changes nothing, unless said otherwise.
- * Workspaces are 256-byte aligned and zeroed once before their first use.  One
- * workspace serves one stream at a time: calls that may overlap take one each, and
- * calls that change one cache are ordered by the caller.
+ * Workspaces are 256-byte aligned; the first 256 bytes are zeroed once before the first
+ * use, the rest may hold anything.  One workspace, large enough for each, may serve several
+ * caches, and both the page operators and the scorer (but not the calls of hstu.h as well),
+ * one stream at a time: calls that may overlap take one each, and calls that change one
+ * cache are ordered by the caller.
  */
 #ifndef HSTU_CACHE_B200_H
 #define HSTU_CACHE_B200_H

@@ -62,7 +62,11 @@ constexpr int kNarrow = 64, kWide = 128;   // nodes of a group in the two forms
 // tree_finish.  The last CTA of tree_attn sets kVerdict and clears the others for the next call.
 // They lie in `pad`, which nothing else writes, so that a workspace may serve the page operators
 // (which leave valid = 1) and the scorer in turn.
-enum { kItems = 0, kTaken = 1, kBad = 2, kDone = 3, kVerdict = 4 };
+// The items are counted in 64 bits: where offsets are bad, trees may overlap, and a million of
+// them claim more than 2^31 items (64 heads, 8192 nodes each) before the call is refused.
+enum { kItems = 0, kTaken = 2, kBad = 3, kDone = 4, kVerdict = 5 };
+
+__device__ __forceinline__ unsigned long long* items_claimed(Control* c) { return reinterpret_cast<unsigned long long*>(&c->pad[kItems]); }
 
 // What tree_prep leaves for a tree: its nodes [off, off + m), history length n, live
 // history rows [0, s) and [lo, n), live 128-row tiles [0, ts) and [w0, ceil(n / 128)),
@@ -208,13 +212,13 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeParams p) {
     const int cnt = p.H * groups * t.splits;
     if (tid == 0) {
         p.info[b] = t;
-        int base = bad ? 0 : atomicAdd(&p.ctrl->pad[kItems], cnt);
-        if (bad || (long long)base + cnt > p.max_items) {
+        long long base = bad ? 0 : (long long)atomicAdd(items_claimed(p.ctrl), (unsigned long long)cnt);
+        if (bad || base + cnt > p.max_items) {
             atomicOr(&p.ctrl->status, kStatusBounds);
             atomicExch(&p.ctrl->pad[kBad], -1);
             base = -1;
         }
-        s_base = base;
+        s_base = (int)base;                          // max_items is below 2^31
     }
     __syncthreads();
     if (s_base < 0) return;
@@ -458,7 +462,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     if (warp == kFetchWarp) {
         // ============================================================ work fetch
-        const int n_items = p.ctrl->pad[kBad] == 0 ? p.ctrl->pad[kItems] : 0;
+        const int n_items = p.ctrl->pad[kBad] == 0 ? (int)*items_claimed(p.ctrl) : 0;
         bool ok = true;
         for (int it_use = 0;; it_use++) {
             const int slot = it_use & 1;
@@ -1015,7 +1019,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (atomicAdd(&p.ctrl->pad[kDone], 1) == (int)gridDim.x - 1) {
             __threadfence();
             p.ctrl->pad[kVerdict] = atomicAdd(&p.ctrl->pad[kBad], 0);
-            p.ctrl->pad[kItems] = p.ctrl->pad[kTaken] = p.ctrl->pad[kBad] = p.ctrl->pad[kDone] = 0;
+            *items_claimed(p.ctrl) = 0;
+            p.ctrl->pad[kTaken] = p.ctrl->pad[kBad] = p.ctrl->pad[kDone] = 0;
         }
     }
 }

@@ -116,6 +116,11 @@ class Layer:
         self.n_static, self.n_realtime = n_static, n_realtime
         self.dims = make_dims(self.T, self.B, H, d, dtype, alpha, max_seq_len, n_pos, n_tbuckets, ln_eps)
         self.mask = make_mask(mask_kind, n_static, n_realtime)
+        if mask_kind == "window":
+            for t, n in ((n_static, "n_static"), (n_realtime, "n_realtime")):
+                _on(t, n, seq_offsets.device, torch.int32)
+                if t.numel() != self.B:
+                    raise ValueError(f"{n} must have one entry for each of the {self.B} rows")
         self.norm = None
         if n_groups > 1:
             _need(token_group, "token_group", torch.uint8)

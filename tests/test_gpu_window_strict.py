@@ -98,3 +98,17 @@ def test_bias_gradients_of_extreme_times(d):
         assert_bf16(got[n], r, n, bf16(m))
     for n, r in zip(("d_rab_pos", "d_rab_time"), ref[3:]):
         assert errors(got[n], r)[0] <= 2e-5, n
+
+
+def test_rules_of_other_batches_are_refused():
+    """Sinks and windows for fewer or more rows than the batch has: the device would read past them."""
+    from hstu_jagged_pointwise_b200 import ops
+    off = torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda")
+    ts = torch.arange(9, dtype=torch.int64, device="cuda")
+    rule = lambda n: torch.ones(n, dtype=torch.int32, device="cuda")
+    for s, w in ((1, 2), (2, 1), (3, 2), (2, 3), (0, 2)):
+        with pytest.raises(ValueError):
+            ops.Layer(off, ts, 1, 64, torch.bfloat16, 5.0, 5, mask_kind="window", n_static=rule(s), n_realtime=rule(w))
+        with pytest.raises(ValueError):
+            ops.HSTULayer(off, ts, 64, 1, 64, 5.0, 5, mask_kind="window", n_static=rule(s), n_realtime=rule(w))
+    ops.Layer(off, ts, 1, 64, torch.bfloat16, 5.0, 5, mask_kind="window", n_static=rule(2), n_realtime=rule(2))

@@ -137,7 +137,9 @@ __device__ void refuse(const PlanParams& p, int bit) {
     }
 }
 
-// The first `want` free pages, lowest first, into free_list; false when there are fewer.
+// The first `want` free pages, lowest first, into free_list; false when there are fewer.  From page
+// 0, 4096 pages a round, so a pool whose low pages are held costs the walk through them: append + free
+// of three rows 12.5 us where the first page is free, 33 behind 90,000 held pages, 221 behind 900,000.
 __device__ bool find_free(const PlanParams& p, int want, int* s_warp, int* s_total) {
     int found = 0;
     for (int p0 = 0; p0 < p.c.n_pages && found < want; p0 += 4 * kPlanThreads) {

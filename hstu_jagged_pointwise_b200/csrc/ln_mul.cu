@@ -93,7 +93,10 @@ __device__ __forceinline__ void load_f32v(const float* base, int c, int n, float
 }
 
 // The next row's Y and U are on their way while this row's two sums meet: 20000 rows of 1024
-// bf16 26.4 -> 22.1 us (5.6 TB/s), 25000 of 512 16.5 -> 14.2, 8000 of 4096 73 -> 43.5.
+// bf16 26.4 -> 22.1 us (5.6 TB/s), 25000 of 512 16.5 -> 14.2, 8000 of 4096 73 -> 43.5.  It pays at the
+// widest rows too, though they spill with it (468 bytes a thread against 72 without): 16000 of 8192
+// 394 -> 267 us, 2400 65.4 -> 54.1, 16000 of 4608 243 -> 171; with one row a block or two, where there is
+// next to nothing to fetch ahead, 700 of 8192 17.4 to 18.8 -> 18.5, 700 of 4608 11.8 -> 12.3.
 template <typename T, int WPR, int NCW>
 __global__ void __launch_bounds__(32 * WPR) ln_fwd_kernel(LnParams p) {
     constexpr int V = Vec<T>::N;

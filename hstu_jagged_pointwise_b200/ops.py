@@ -564,7 +564,9 @@ class TreeScorer:
     window mask would let it see.  One-node trees are M-FALCON candidates or a next event.
 
     Reusing a scorer keeps its workspace; the cache may grow between calls (lengths are read on
-    the device at each call).  One scorer serves one stream at a time."""
+    the device at each call), and slots, node_offsets, parent, node_ts, n_sink and window may be
+    changed in place while B, T and max_nodes hold: a beam search with as many nodes at each step
+    copies its new trees into the tensors that it gave.  One scorer serves one stream at a time."""
 
     def __init__(self, cache: PagedCache, slots, node_offsets, parent, node_ts, H: int, d: int, alpha: float,
                  max_nodes: int, n_sink: Optional[torch.Tensor] = None, window: Optional[torch.Tensor] = None,

@@ -50,6 +50,7 @@
  *    inside `workspace`; the affected launch then does no work.  Read and
  *    clear it with hstu_check_device_error().
  *  - Alignment: every tensor pointer 16-byte aligned; H*d*elem_size a multiple of 16.
+ *  - Outputs overlap neither the inputs nor each other.
  *  - Supported: dtype HSTU_BF16 with d_qk = d_v in {64, 128}; dtype HSTU_F32 with
  *    d_qk = d_v in {32, 64, 128}; P in [1, 1024]; nb in [1, 64]; H >= 1; H*d_v <= 8192
  *    (<= 4096 for HSTU_F32);
@@ -445,7 +446,10 @@ HSTU_API const char* hstu_status_string(int status);
  * launches[k] and total_ms[k] for kernel kinds k < n_kinds (host arrays);
  * it returns the number of kinds the library knows, or a negative status.
  * hstu_profile_kind_name(k) names kind k ("" when out of range).  Meant for
- * benchmarks: recording costs two event records per launch. */
+ * benchmarks: recording costs two event records per launch.  "dq_convert_kernel" is
+ * the launch after the attention backward: dQ to its type, the sums of the bias
+ * gradients and, for HSTU_MASK_WINDOW, of the sinks' keys.  The kernels of
+ * hstu_cache.h are not recorded. */
 HSTU_API int hstu_profile_enable(int32_t on);
 HSTU_API int hstu_profile_read(int32_t n_kinds, int32_t* launches, double* total_ms);
 HSTU_API const char* hstu_profile_kind_name(int32_t kind);

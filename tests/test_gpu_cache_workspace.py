@@ -127,3 +127,28 @@ def test_workspace_need_not_be_clear():
     got = s.score(*case.tensors())
     assert s.check_device_error() == OK
     assert torch.equal(got["y"], want["y"]) and torch.equal(got["o_pre"], want["o_pre"])
+
+
+def test_trees_changed_in_place():
+    """A scorer whose tensors get other trees, slots and rules, called and replayed, equals a new one."""
+    rule = ([0, 4, 2], [30, 100, 5])
+    case = Case([40, 129, 300], [6, 70, 20], 2, 64, 16, rule=rule, seed=9)
+    s = case.scorer()
+    x = case.tensors()
+    first = s.score(*x)
+    g, out = torch.cuda.CUDAGraph(), {n: torch.empty_like(t) for n, t in first.items()}
+    with torch.cuda.graph(g):
+        s.score(*x, out=out)
+    other = Case([40, 129, 300], [25, 1, 70], 2, 64, 16, shape="chain", rule=([1, 0, 3], [400, 7, 64]), slots=[2, 0, 1], seed=9)
+    for name, new in (("slots", other.slots), ("node_offsets", other.off), ("parent", other.parent), ("node_ts", other.node_ts),
+                      ("n_sink", other.S), ("window", other.Wn)):
+        getattr(s, name).copy_(torch.as_tensor(new))
+    new = other.scorer()
+    want = new.score(*x)
+    g.replay()
+    again = s.score(*x)
+    assert s.check_device_error() == OK and new.check_device_error() == OK
+    for n, t in want.items():
+        assert torch.equal(again[n], t) and torch.equal(out[n], t), n
+    assert not torch.equal(first["y"], want["y"])
+    del g
